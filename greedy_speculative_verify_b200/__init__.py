@@ -31,7 +31,14 @@ EXPORTS = (
     "vg_embed_rows", "vg_spec_rows", "vg_spec_commit", "vg_spec_rows_given",
     "vg_mtp_workspace_bytes", "vg_mtp_draft", "vg_attn_workspace_bytes", "vg_attn_verify",
     "vg_verify_step_small_workspace_bytes", "vg_verify_step_small",
+    "vg_kv8_append", "vg_kv8_read", "vg_kv8_attn_workspace_bytes", "vg_kv8_attn",
+    "vg_attn_verify_kv8_workspace_bytes", "vg_attn_verify_kv8",
+    "vg_token_logprobs_workspace_bytes", "vg_token_logprobs",
 )
+
+# vg_kv8 formats and output element types
+VG_KV8_INT8, VG_KV8_E4M3 = 0, 1
+VG_BF16, VG_F32 = 0, 1
 
 # vg_kernel
 VG_KERNEL_ROUTER, VG_KERNEL_GROUPING, VG_KERNEL_EXPERTS = 0, 1, 2
@@ -70,6 +77,12 @@ class vg_mtp_weights(ctypes.Structure):
                 ("lm_head", ctypes.c_void_p), ("V", ctypes.c_int32)]
 
 
+class vg_kv8(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("B", ctypes.c_int32), ("L_max", ctypes.c_int32), ("n_kv", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("block", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_amax", ctypes.c_void_p), ("v_amax", ctypes.c_void_p)]
+
+
 MOE_DIMS = vg_moe_dims(1280, 896, 64, 2, 6)
 
 _lib = None
@@ -85,6 +98,7 @@ def load():
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, u64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64, ctypes.c_size_t
     dims_p = ctypes.POINTER(vg_moe_dims)
+    kv8_p, i64 = ctypes.POINTER(vg_kv8), ctypes.c_int64
     sig = {
         "vg_status_string": (ctypes.c_char_p, [i32]),
         "vg_abi_version": (i32, []),
@@ -114,6 +128,14 @@ def load():
         "vg_verify_step_small": (i32, [dims_p, i32, i32, i32, vp, ctypes.POINTER(vp), ctypes.POINTER(vp),
                                        ctypes.POINTER(vp), ctypes.POINTER(vp), vp, i32, vp, vp, vp, vp, vp, vp,
                                        vp, sz, vp]),
+        "vg_kv8_append": (i32, [kv8_p, i32, vp, i64, vp, i64, vp, vp, vp]),
+        "vg_kv8_read": (i32, [kv8_p, i32, vp, vp, i32, vp, i64, vp, i64, vp]),
+        "vg_kv8_attn_workspace_bytes": (sz, [kv8_p, i32, i32]),
+        "vg_kv8_attn": (i32, [kv8_p, i32, i32, vp, i64, vp, vp, vp, ctypes.c_float, vp, i64, vp, sz, vp]),
+        "vg_attn_verify_kv8_workspace_bytes": (sz, [kv8_p, i32]),
+        "vg_attn_verify_kv8": (i32, [kv8_p, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "vg_token_logprobs_workspace_bytes": (sz, [i32, i32, i32, i32]),
+        "vg_token_logprobs": (i32, [i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -331,3 +353,168 @@ def vg_attn_verify(B, K, x, w_qkv, w_o, kv_cache, lens, out, workspace, o_out=No
     _check(load().vg_attn_verify(B, K, kv_cache.shape[2], _ptr(x), _ptr(w_qkv), _ptr(w_o), _ptr(kv_cache), _ptr(lens),
                                  _ptr(out), _ptr(o_out), _ptr(workspace), workspace.numel(), _stream(stream)),
            "vg_attn_verify")
+
+
+# ------------------------------------------------------------ 8-bit KV cache
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(device, **tensors):
+    """Every tensor given lies on that device, and it is the current one (the
+    library launches on the current device)."""
+    import torch
+
+    if device.type == "cuda":
+        _need(device.index == torch.cuda.current_device(), f"tensors are on {device}, which is not the current device")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _rows(name, t, n, width, dtypes):
+    """Row stride of a [n, width] matrix with dense rows."""
+    if t is None:
+        return 0
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be [{n}, {width}] of {dtypes}, got {tuple(t.shape)} of {t.dtype}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows")
+    return t.stride(0) if n > 1 else max(t.stride(0), width)
+
+
+def _dense(name, t, shape, dtype):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError(f"{name} must be dense {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+
+
+def _bytes_of(workspace):
+    if workspace is None:
+        return 0
+    _need(workspace.is_contiguous(), "workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
+def make_kv8(k, v, k_amax, v_amax):
+    """vg_kv8 over caller-owned device tensors: k and v [B, n_kv, L_max, dim] of
+    codes (torch.int8 or torch.float8_e4m3fn; inside a (sequence, head) they lie
+    in the order include/vgv.h documents), k_amax and v_amax fp32
+    [B, n_kv, L_max / block]. The handle keeps the tensors alive."""
+    import torch
+
+    formats = {torch.int8: VG_KV8_INT8, torch.float8_e4m3fn: VG_KV8_E4M3}
+    _need(k.dim() == 4 and k.dtype in formats, "k must be [B, n_kv, L_max, dim] of int8 or float8_e4m3fn")
+    B, n_kv, L_max, dim = k.shape
+    _dense("k", k, k.shape, k.dtype)
+    _dense("v", v, k.shape, k.dtype)
+    _need(k_amax.dim() == 3 and k_amax.shape[2] > 0 and L_max % k_amax.shape[2] == 0,
+          "k_amax must be [B, n_kv, L_max / block]")
+    for name, t in (("k_amax", k_amax), ("v_amax", v_amax)):
+        _dense(name, t, (B, n_kv, k_amax.shape[2]), torch.float32)
+    for name, t in (("v", v), ("k_amax", k_amax), ("v_amax", v_amax)):
+        _need(t.device == k.device, f"{name} is on {t.device}, not on {k.device}")
+    c = vg_kv8(formats[k.dtype], B, L_max, n_kv, dim, L_max // k_amax.shape[2], k.data_ptr(), v.data_ptr(),
+               k_amax.data_ptr(), v_amax.data_ptr())
+    c.tensors = (k, v, k_amax, v_amax)
+    c.device = k.device
+    return c
+
+
+def vg_kv8_append(cache, rows, k, v, pos, n_new=None, stream=None):
+    """Quantises `rows` new rows per sequence (k, v: bf16 [B * rows, n_kv * dim],
+    any row stride) into the cache at positions pos[b] .. (the first n_new[b])."""
+    import torch
+
+    B, width, bf16 = cache.B, cache.n_kv * cache.dim, (torch.bfloat16,)
+    ks, vs = _rows("k", k, B * rows, width, bf16), _rows("v", v, B * rows, width, bf16)
+    _dense("pos", pos, (B,), torch.int32)
+    _dense("n_new", n_new, (B,), torch.int32)
+    _on(cache.device, k=k, v=v, pos=pos, n_new=n_new)
+    _check(load().vg_kv8_append(ctypes.byref(cache), rows, _ptr(k), ks, _ptr(v), vs, _ptr(pos), _ptr(n_new),
+                                _stream(stream)), "vg_kv8_append")
+
+
+def vg_kv8_read(cache, rows, pos, k_out, v_out, n_rows=None, stream=None):
+    """Positions pos[b] .. pos[b] + n_rows[b] - 1 of every sequence as values, into
+    rows b * rows .. of k_out and v_out ([B * rows, n_kv * dim], bf16 or fp32
+    alike; either may be None)."""
+    import torch
+
+    B, width, types = cache.B, cache.n_kv * cache.dim, (torch.bfloat16, torch.float32)
+    ks, vs = _rows("k_out", k_out, B * rows, width, types), _rows("v_out", v_out, B * rows, width, types)
+    _need(k_out is None or v_out is None or k_out.dtype == v_out.dtype, "k_out and v_out must have one type")
+    _dense("pos", pos, (B,), torch.int32)
+    _dense("n_rows", n_rows, (B,), torch.int32)
+    _on(cache.device, k_out=k_out, v_out=v_out, pos=pos, n_rows=n_rows)
+    out = k_out if k_out is not None else v_out
+    kind = VG_F32 if out is not None and out.dtype == torch.float32 else VG_BF16
+    _check(load().vg_kv8_read(ctypes.byref(cache), rows, _ptr(pos), _ptr(n_rows), kind, _ptr(k_out), ks, _ptr(v_out), vs,
+                              _stream(stream)), "vg_kv8_read")
+
+
+def vg_kv8_attn_workspace_bytes(cache, rows, n_heads):
+    return load().vg_kv8_attn_workspace_bytes(ctypes.byref(cache), rows, n_heads)
+
+
+def vg_kv8_attn(cache, rows, n_heads, q, lens, scale, o, workspace, first=None, n_new=None, stream=None):
+    """Attention of `rows` query rows per sequence (q, o: bf16 [B * rows,
+    n_heads * dim], any row stride) over the cache."""
+    import torch
+
+    B, width, bf16 = cache.B, n_heads * cache.dim, (torch.bfloat16,)
+    qs, os_ = _rows("q", q, B * rows, width, bf16), _rows("o", o, B * rows, width, bf16)
+    _dense("lens", lens, (B,), torch.int32)
+    _dense("first", first, (B,), torch.int32)
+    _dense("n_new", n_new, (B,), torch.int32)
+    _on(cache.device, q=q, o=o, lens=lens, first=first, n_new=n_new, workspace=workspace)
+    _check(load().vg_kv8_attn(ctypes.byref(cache), rows, n_heads, _ptr(q), qs, _ptr(lens), _ptr(first), _ptr(n_new), scale,
+                              _ptr(o), os_, _ptr(workspace), _bytes_of(workspace), _stream(stream)), "vg_kv8_attn")
+
+
+def vg_attn_verify_kv8_workspace_bytes(cache, K):
+    return load().vg_attn_verify_kv8_workspace_bytes(ctypes.byref(cache), K)
+
+
+def vg_attn_verify_kv8(cache, K, x, w_qkv, w_o, lens, out, workspace, o_out=None, stream=None):
+    """One attention layer of a verify step on an 8-bit cache (vg_attn_verify's
+    arguments; the batch is the cache's)."""
+    import torch
+
+    R, H, bf16 = cache.B * (K + 1), cache.n_kv * cache.dim, torch.bfloat16
+    for name, t, shape in (("x", x, (R, H)), ("w_qkv", w_qkv, (3 * H, H)), ("w_o", w_o, (H, H)), ("out", out, (R, H)),
+                           ("o_out", o_out, (R, H))):
+        _dense(name, t, shape, bf16)
+    _dense("lens", lens, (cache.B,), torch.int32)
+    _on(cache.device, x=x, w_qkv=w_qkv, w_o=w_o, lens=lens, out=out, o_out=o_out, workspace=workspace)
+    _check(load().vg_attn_verify_kv8(ctypes.byref(cache), K, _ptr(x), _ptr(w_qkv), _ptr(w_o), _ptr(lens), _ptr(out),
+                                     _ptr(o_out), _ptr(workspace), _bytes_of(workspace), _stream(stream)),
+           "vg_attn_verify_kv8")
+
+
+# ------------------------------------------------------------ log probabilities
+def vg_token_logprobs_workspace_bytes(R, H, V, n_top):
+    return load().vg_token_logprobs_workspace_bytes(R, H, V, n_top)
+
+
+def vg_token_logprobs(h, lm_head, tokens, logprob, entropy, top_ids, top_logprobs, workspace, stream=None):
+    """Log probabilities of tokens[r] after hidden row h[r], the entropy and the
+    top_ids.shape[1] most likely tokens of each row; tokens with logprob, entropy,
+    and top_ids with top_logprobs may be None."""
+    import torch
+
+    _need(h.dim() == 2 and lm_head.dim() == 2, "h must be [R, H], lm_head [V, H]")
+    (R, H), V = h.shape, lm_head.shape[0]
+    n_top = 0 if top_ids is None else top_ids.shape[-1]
+    _dense("h", h, (R, H), torch.bfloat16)
+    _dense("lm_head", lm_head, (V, H), torch.bfloat16)
+    _dense("tokens", tokens, (R,), torch.int32)
+    _dense("logprob", logprob, (R,), torch.float32)
+    _dense("entropy", entropy, (R,), torch.float32)
+    _dense("top_ids", top_ids, (R, n_top), torch.int32)
+    _dense("top_logprobs", top_logprobs, (R, n_top), torch.float32)
+    _on(h.device, lm_head=lm_head, tokens=tokens, logprob=logprob, entropy=entropy, top_ids=top_ids,
+        top_logprobs=top_logprobs, workspace=workspace)
+    _check(load().vg_token_logprobs(R, H, V, _ptr(h), _ptr(lm_head), _ptr(tokens), n_top, _ptr(logprob), _ptr(entropy),
+                                    _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace), _bytes_of(workspace),
+                                    _stream(stream)), "vg_token_logprobs")

@@ -84,7 +84,9 @@ __global__ void __launch_bounds__(256) attn_residual(const __nv_bfloat16* __rest
   reinterpret_cast<uint2*>(out)[c] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-// One thread per (row, pair) of q and of k.
+// One thread per (row, pair) of q and of k. ROWS: the rotated q and k and v go to
+// rows [B*K1, 3H] at a.q instead (the rows an 8-bit cache is written from).
+template <bool ROWS = false>
 __global__ void __launch_bounds__(256) attn_rope_append(const AttnArgs a) {
   griddep_launch_dependents();
   griddep_wait();
@@ -113,6 +115,14 @@ __global__ void __launch_bounds__(256) attn_rope_append(const AttnArgs a) {
     dst[2 * pr] = __float2bfloat16_rn((float)y0);
     dst[2 * pr + 1] = __float2bfloat16_rn((float)y1);
   };
+  if constexpr (ROWS) {
+    __nv_bfloat16* dst = a.q + (size_t)r * 3 * H;
+    turn(0, dst);
+    turn(H, dst + H);
+    dst[2 * H + 2 * pr] = __float2bfloat16_rn(val(2 * H + 2 * pr));
+    dst[2 * H + 2 * pr + 1] = __float2bfloat16_rn(val(2 * H + 2 * pr + 1));
+    return;
+  }
   turn(0, a.q + (size_t)r * H);
   __nv_bfloat16* kc = a.cache + ((size_t)b * 2 * a.L_max + (L + i)) * H;
   __nv_bfloat16* vc = a.cache + ((size_t)(b * 2 + 1) * a.L_max + (L + i)) * H;

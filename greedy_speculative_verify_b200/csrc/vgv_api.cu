@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <mutex>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
@@ -14,12 +15,15 @@
 #include "decode_loop.cuh"
 #include "mtp.cuh"
 #include "attention.cuh"
+#include "kv8.cuh"
+#include "kv8_attn.cuh"
 #include "proj_tc.cuh"
 #include "gemm_moe.cuh"
 #include "gemm_tm.cuh"
 #include "layer_entry.cuh"
 #include "entry_small.cuh"
 #include "lmhead.cuh"
+#include "logprobs.cuh"
 #include "router.cuh"
 #include "step_small.cuh"
 #include "sort.cuh"
@@ -28,6 +32,7 @@ namespace {
 
 constexpr int kH = 1280, kI = 896, kE = 64, kS = 2, kTopK = 6;
 constexpr int kMaxDevices = 64;
+constexpr int kMaxSmemBytes = 232448;  // shared memory a CTA can ask for (227 KB)
 constexpr int kEntryMaxGrid = 256;  // CTAs of the layer-entry kernel at most
 
 // Bytes of expert weights the layer entry prefetches into L2: the gate|up rows
@@ -145,6 +150,8 @@ vg_status device_state(DevState** out) {
     if (cudaFuncSetAttribute(vg::lmhead_argmax_accept, cudaFuncAttributeMaxDynamicSharedMemorySize, vg::kLmSmemBytes) !=
         cudaSuccess)
       return cuda_fail();
+    if (cudaFuncSetAttribute(vg::logprob_tiles, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes) != cudaSuccess)
+      return cuda_fail();
     // Kernels that follow each other with dependent launches share SMs only if
     // their shared-memory configurations agree: every kernel of the decode
     // chain asks for the largest shared-memory carveout.
@@ -160,6 +167,7 @@ vg_status device_state(DevState** out) {
           cudaFuncSetAttribute(vg::moe_combine<true>, kC, kMax) != cudaSuccess ||
           cudaFuncSetAttribute(vg::moe_combine<false>, kC, kMax) != cudaSuccess ||
           cudaFuncSetAttribute(vg::lmhead_argmax_accept, kC, kMax) != cudaSuccess ||
+          cudaFuncSetAttribute(vg::logprob_tiles, kC, kMax) != cudaSuccess ||
           cudaFuncSetAttribute(vg::embed_rows, kC, kMax) != cudaSuccess ||
           cudaFuncSetAttribute(vg::spec_rows, kC, kMax) != cudaSuccess ||
           cudaFuncSetAttribute(vg::spec_rows_given, kC, kMax) != cudaSuccess ||
@@ -195,6 +203,8 @@ vg_status make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* d
 int box_rows(int64_t rows, int full) { return rows >= full ? full : (int)((rows + 7) / 8 * 8); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
@@ -1141,6 +1151,25 @@ AttnWs attn_layout(int B, int K, int L_max) {
   L.total = off;
   return L;
 }
+// act W^T as fp32 partial sums over the 5 slices of the reduction, on the tensor cores
+cudaError_t attn_project(const void* act, const void* wgt, int R, int n_out, float* pk, cudaStream_t s) {
+  using namespace vg;
+  CUtensorMap mW, mX;
+  const uint64_t dW[2] = {kH, (uint64_t)n_out}, dX[2] = {kH, (uint64_t)R}, sK[1] = {kH * 2};
+  const uint32_t bW[2] = {kBK, kBM}, bX[2] = {kBK, (uint32_t)box_rows(R, kPtRows)};
+  if (make_map(&mW, wgt, 2, dW, sK, bW) || make_map(&mX, act, 2, dX, sK, bX)) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t pc = {};  // 3-d grid: (128 outputs, 256-wide reduction slice, 128 rows)
+  pc.gridDim = dim3(n_out / kBM, kProjSplits, cdiv(R, kPtRows));
+  pc.blockDim = dim3(192);
+  pc.dynamicSmemBytes = kPtSmemBytes;
+  pc.stream = s;
+  cudaLaunchAttribute pa[1];
+  pa[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pa[0].val.programmaticStreamSerializationAllowed = 1;
+  pc.attrs = pa;
+  pc.numAttrs = 1;
+  return cudaLaunchKernelEx(&pc, attn_proj_tc, mW, mX, R, n_out, (int)bX[1], pk);
+}
 }  // namespace
 
 extern "C" size_t vg_attn_workspace_bytes(int32_t B, int32_t K, int32_t L_max) {
@@ -1176,24 +1205,7 @@ extern "C" vg_status vg_attn_verify(int32_t B, int32_t K, int32_t L_max, const v
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   auto bf = [&](size_t o) { return reinterpret_cast<__nv_bfloat16*>(ws + o); };
   float* pk = reinterpret_cast<float*>(ws + L.pk);
-  // x W^T as fp32 partial sums over the 5 slices of the reduction, on the tensor cores
-  auto launch_proj = [&](const void* act, const void* wgt, int n_out) {
-    CUtensorMap mW, mX;
-    const uint64_t dW[2] = {kH, (uint64_t)n_out}, dX[2] = {kH, (uint64_t)R}, sK[1] = {kH * 2};
-    const uint32_t bW[2] = {kBK, kBM}, bX[2] = {kBK, (uint32_t)box_rows(R, kPtRows)};
-    if (make_map(&mW, wgt, 2, dW, sK, bW) || make_map(&mX, act, 2, dX, sK, bX)) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t pc = {};  // 3-d grid: (128 outputs, 256-wide reduction slice, 128 rows)
-    pc.gridDim = dim3(n_out / kBM, kProjSplits, cdiv(R, kPtRows));
-    pc.blockDim = dim3(192);
-    pc.dynamicSmemBytes = kPtSmemBytes;
-    pc.stream = s;
-    cudaLaunchAttribute pa[1];
-    pa[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pa[0].val.programmaticStreamSerializationAllowed = 1;
-    pc.attrs = pa;
-    pc.numAttrs = 1;
-    return cudaLaunchKernelEx(&pc, attn_proj_tc, mW, mX, R, n_out, (int)bX[1], pk);
-  };
+  auto launch_proj = [&](const void* act, const void* wgt, int n_out) { return attn_project(act, wgt, R, n_out, pk, s); };
   // q/k/v = x W_qkv^T as split partial sums
   if (launch_proj(x, w_qkv, 3 * kH) != cudaSuccess) return cuda_fail();
   AttnArgs a{};
@@ -1208,7 +1220,7 @@ extern "C" vg_status vg_attn_verify(int32_t B, int32_t K, int32_t L_max, const v
   a.part = reinterpret_cast<float*>(ws + L.part);
   a.n_chunks = cdiv(L_max, kAttnChunk);
   a.o = o_out ? static_cast<__nv_bfloat16*>(o_out) : bf(L.o);
-  if (launch_dep(attn_rope_append, cdiv(R * kH / 2, 256), 256, 0, s, Launch::kPlain, a) != cudaSuccess)
+  if (launch_dep(attn_rope_append<false>, cdiv(R * kH / 2, 256), 256, 0, s, Launch::kPlain, a) != cudaSuccess)
     return cuda_fail();
   cudaLaunchConfig_t cfg = {};  // 2-d grid: (sequence x head, chunk)
   cfg.gridDim = dim3(B * kAttnHeads, a.n_chunks);
@@ -1230,6 +1242,423 @@ extern "C" vg_status vg_attn_verify(int32_t B, int32_t K, int32_t L_max, const v
   if (launch_dep(attn_residual, cdiv(R * kH / 4, 256), 256, 0, s, Launch::kPlain, static_cast<const __nv_bfloat16*>(x),
                  (const float*)pk, kProjSplits, R * kH, static_cast<__nv_bfloat16*>(out)) != cudaSuccess)
     return cuda_fail();
+  return VG_OK;
+}
+
+// ------------------------------------------------------------ 8-bit KV cache
+namespace {
+
+// The cache's own fields: shape, pointers, alignment.
+vg_status kv8_check(const vg_kv8* c) {
+  if (c == nullptr || c->B < 0 || c->L_max < 1 || c->n_kv < 1) return VG_ERR_INVALID_ARG;
+  if ((c->format != VG_KV8_INT8 && c->format != VG_KV8_E4M3) || (c->dim != 64 && c->dim != 128) ||
+      (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) || c->L_max > (1 << 20) || c->n_kv > 1024)
+    return VG_ERR_UNSUPPORTED;
+  if (c->L_max % c->block != 0) return VG_ERR_INVALID_ARG;
+  if (c->B == 0) return VG_OK;
+  if (!c->k || !c->v || !c->k_amax || !c->v_amax || !aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_amax) ||
+      !aligned4(c->v_amax))
+    return VG_ERR_INVALID_ARG;
+  return VG_OK;
+}
+
+size_t kv8_code_bytes(const vg_kv8* c) { return (size_t)c->B * c->n_kv * c->L_max * c->dim; }
+
+bool kv8_overlaps(const vg_kv8* c, const void* p, size_t bytes) {
+  const size_t codes = kv8_code_bytes(c), am = (size_t)c->B * c->n_kv * (c->L_max / c->block) * 4;
+  return p != nullptr && (overlaps(c->k, codes, p, bytes) || overlaps(c->v, codes, p, bytes) ||
+                          overlaps(c->k_amax, am, p, bytes) || overlaps(c->v_amax, am, p, bytes));
+}
+
+vg::Kv8View kv8_view(const vg_kv8* c) {
+  return vg::Kv8View{c->B,     c->L_max, c->n_kv, c->block, static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v),
+                     c->k_amax, c->v_amax};
+}
+
+// Bytes that n rows of `width` elements, `stride` apart, span.
+size_t rows_span(int64_t n, int64_t stride, int64_t width, int elem) {
+  return n > 0 ? (size_t)((n - 1) * stride + width) * elem : 0;
+}
+
+// Whether two sets of n rows share a byte. Rows of the same stride may lie
+// beside each other, as columns of one matrix.
+bool rows_collide(const void* p, int64_t sp, const void* q, int64_t sq, int64_t n, int64_t wp, int64_t wq, int elem) {
+  if (!overlaps(p, rows_span(n, sp, wp, elem), q, rows_span(n, sq, wq, elem))) return false;
+  const int64_t bytes = static_cast<const char*>(q) - static_cast<const char*>(p);
+  if (sp != sq || bytes % elem != 0) return true;
+  int64_t d = bytes / elem % sp;
+  if (d < 0) d += sp;
+  return d < wp || d + wq > sp;
+}
+
+// Calls f with the format and head width as template arguments.
+template <typename F>
+cudaError_t kv8_dispatch(int32_t format, int32_t dim, F&& f) {
+  using I = std::integral_constant<int, vg::kKv8Int8>;
+  using E = std::integral_constant<int, vg::kKv8E4m3>;
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (format == VG_KV8_INT8) return dim == 64 ? f(I{}, D64{}) : f(I{}, D128{});
+  return dim == 64 ? f(E{}, D64{}) : f(E{}, D128{});
+}
+
+// Query rows of a kv head per tile of the attention kernel, in 8-row columns:
+// one column of tensor-core tiles for up to 8 rows, else two.
+int kv8_nt(int rows, int group) { return rows * group <= 8 ? 1 : 2; }
+
+size_t kv8_attn_ws(const vg_kv8* c, int rows, int n_heads) {
+  const int group = n_heads / c->n_kv, nt = kv8_nt(rows, group), tiles = vg::cdiv(rows * group, 8 * nt);
+  return align256((size_t)c->B * c->n_kv * tiles * vg::cdiv(c->L_max, vg::kKaChunk) * 8 * nt * (2 + c->dim) * 4);
+}
+
+vg_status kv8_attn_check(const vg_kv8* c, int32_t rows, int32_t n_heads) {
+  const vg_status st = kv8_check(c);
+  if (st != VG_OK) return st;
+  if (rows < 1 || n_heads < 1 || n_heads % c->n_kv != 0) return VG_ERR_INVALID_ARG;
+  if (rows > vg::kKaMaxRows || n_heads / c->n_kv > vg::kKaMaxGroup) return VG_ERR_UNSUPPORTED;
+  const int group = n_heads / c->n_kv, nt = kv8_nt(rows, group);
+  if ((int64_t)c->B * c->n_kv * vg::cdiv(rows * group, 8 * nt) * 8 * nt >= ((int64_t)1 << 31)) return VG_ERR_UNSUPPORTED;
+  return VG_OK;
+}
+
+vg_status kv8_append_launch(const vg_kv8* c, int32_t rows, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, const int32_t* pos, const int32_t* n_new, cudaStream_t s) {
+  using namespace vg;
+  Kv8AppendArgs a{};
+  a.c = kv8_view(c);
+  a.rows = rows;
+  a.nb = (rows + c->block - 2) / c->block + 1;
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.pos = pos;
+  a.n_new = n_new;
+  const int grid = c->B * c->n_kv * a.nb * 2, units = c->block * c->dim / 16;
+  const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
+    constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
+    if (units <= 256) return launch_dep(kv8_append<F, D, 1>, grid, units, 0, s, Launch::kPlain, a);
+    if (units <= 512) return launch_dep(kv8_append<F, D, 2>, grid, 256, 0, s, Launch::kPlain, a);
+    return launch_dep(kv8_append<F, D, 4>, grid, 256, 0, s, Launch::kPlain, a);
+  });
+  return e == cudaSuccess ? VG_OK : cuda_fail();
+}
+
+vg_status kv8_attn_launch(const vg_kv8* c, int32_t rows, int32_t n_heads, const void* q, int64_t q_stride,
+                          const int32_t* lens, const int32_t* first, const int32_t* n_new, float scale, void* o,
+                          int64_t o_stride, void* workspace, cudaStream_t s) {
+  using namespace vg;
+  const int group = n_heads / c->n_kv, nt = kv8_nt(rows, group);
+  Kv8AttnArgs a{};
+  a.c = kv8_view(c);
+  a.rows = rows;
+  a.n_heads = n_heads;
+  a.n_tiles = cdiv(rows * group, 8 * nt);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
+  a.lens = lens;
+  a.first = first;
+  a.n_new = n_new;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634 / (c->format == VG_KV8_INT8 ? 127.0 : 448.0));
+  a.part = static_cast<float*>(workspace);
+  a.n_chunks = cdiv(c->L_max, kKaChunk);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.o_stride = o_stride;
+  const int units = c->B * c->n_kv * a.n_tiles;
+  auto chunks = [&](auto kern) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(units, a.n_chunks);
+    cfg.blockDim = dim3(32 * kKaWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+  };
+  const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
+    constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
+    cudaError_t r;
+    {
+      ProfScope ps(VG_KERNEL_ATTENTION, s);
+      r = nt == 1 ? chunks(kv8_attn_chunk<F, D, 1>) : chunks(kv8_attn_chunk<F, D, 2>);
+    }
+    if (r != cudaSuccess) return r;
+    return nt == 1 ? launch_dep(kv8_attn_merge<D, 1>, units * 8, D, 0, s, Launch::kPlain, a)
+                   : launch_dep(kv8_attn_merge<D, 2>, units * 16, D, 0, s, Launch::kPlain, a);
+  });
+  return e == cudaSuccess ? VG_OK : cuda_fail();
+}
+
+}  // namespace
+
+extern "C" vg_status vg_kv8_append(const vg_kv8* c, int32_t rows, const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, const int32_t* pos, const int32_t* n_new, vg_stream_t stream) {
+  vg_status st = kv8_check(c);
+  if (st != VG_OK) return st;
+  if (rows < 0) return VG_ERR_INVALID_ARG;
+  if (rows > (1 << 20)) return VG_ERR_UNSUPPORTED;
+  if (c->B == 0 || rows == 0) return VG_OK;
+  const int64_t width = (int64_t)c->n_kv * c->dim, R = (int64_t)c->B * rows;
+  if (!k || !v || !pos || !aligned16(k) || !aligned16(v) || !aligned4(pos) || !aligned4(n_new) || k_stride < width ||
+      v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride > (1 << 24) || v_stride > (1 << 24))
+    return VG_ERR_INVALID_ARG;
+  if ((int64_t)c->B * c->n_kv * ((rows + c->block - 2) / c->block + 1) * 2 >= ((int64_t)1 << 31)) return VG_ERR_UNSUPPORTED;
+  if (kv8_overlaps(c, k, rows_span(R, k_stride, width, 2)) || kv8_overlaps(c, v, rows_span(R, v_stride, width, 2)))
+    return VG_ERR_INVALID_ARG;
+  DevState* dev = nullptr;
+  if ((st = device_state(&dev)) != VG_OK) return st;
+  return kv8_append_launch(c, rows, k, k_stride, v, v_stride, pos, n_new, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" vg_status vg_kv8_read(const vg_kv8* c, int32_t rows, const int32_t* pos, const int32_t* n_rows,
+                                 int32_t out_type, void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
+                                 vg_stream_t stream) {
+  using namespace vg;
+  vg_status st = kv8_check(c);
+  if (st != VG_OK) return st;
+  if (rows < 0 || (out_type != VG_BF16 && out_type != VG_F32)) return VG_ERR_INVALID_ARG;
+  if (rows > (1 << 20)) return VG_ERR_UNSUPPORTED;
+  if (c->B == 0 || rows == 0 || (!k_out && !v_out)) return VG_OK;
+  const int64_t width = (int64_t)c->n_kv * c->dim, R = (int64_t)c->B * rows;
+  const int elem = out_type == VG_F32 ? 4 : 2;
+  auto bad_rows = [&](const void* p, int64_t stride) {
+    return p && (!aligned16(p) || stride < width || stride % 8 != 0 || stride > (1 << 24) ||
+                 kv8_overlaps(c, p, rows_span(R, stride, width, elem)));
+  };
+  if (!pos || !aligned4(pos) || !aligned4(n_rows) || bad_rows(k_out, k_stride) || bad_rows(v_out, v_stride))
+    return VG_ERR_INVALID_ARG;
+  if (k_out && v_out && rows_collide(k_out, k_stride, v_out, v_stride, R, width, width, elem)) return VG_ERR_INVALID_ARG;
+  Kv8ReadArgs a{};
+  a.c = kv8_view(c);
+  a.rows = rows;
+  a.ng = (rows + kKv8Group - 2) / kKv8Group + 1;
+  a.pos = pos;
+  a.n_rows = n_rows;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  const int64_t threads = (int64_t)c->B * c->n_kv * a.ng * c->dim, grid = (threads + 255) / 256;
+  if (grid >= ((int64_t)1 << 31)) return VG_ERR_UNSUPPORTED;
+  DevState* dev = nullptr;
+  if ((st = device_state(&dev)) != VG_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
+    constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
+    return out_type == VG_F32 ? launch_dep(kv8_read<F, D, float>, (int)grid, 256, 0, s, Launch::kPlain, a)
+                              : launch_dep(kv8_read<F, D, __nv_bfloat16>, (int)grid, 256, 0, s, Launch::kPlain, a);
+  });
+  return e == cudaSuccess ? VG_OK : cuda_fail();
+}
+
+extern "C" size_t vg_kv8_attn_workspace_bytes(const vg_kv8* c, int32_t rows, int32_t n_heads) {
+  if (kv8_attn_check(c, rows, n_heads) != VG_OK) return 0;
+  return kv8_attn_ws(c, rows, n_heads);
+}
+
+extern "C" vg_status vg_kv8_attn(const vg_kv8* c, int32_t rows, int32_t n_heads, const void* q, int64_t q_stride,
+                                 const int32_t* lens, const int32_t* first, const int32_t* n_new, float scale, void* o,
+                                 int64_t o_stride, void* workspace, size_t workspace_bytes, vg_stream_t stream) {
+  vg_status st = kv8_attn_check(c, rows, n_heads);
+  if (st != VG_OK) return st;
+  if (c->B == 0) return VG_OK;
+  const int64_t width = (int64_t)n_heads * c->dim, R = (int64_t)c->B * rows;
+  if (!q || !lens || !o || !aligned16(q) || !aligned16(o) || !aligned4(lens) || !aligned4(first) || !aligned4(n_new) ||
+      q_stride < width || o_stride < width || q_stride % 8 != 0 || o_stride % 8 != 0 || q_stride > (1 << 24) ||
+      o_stride > (1 << 24) || !(scale > 0.0f) || !(scale <= 3.0e38f))
+    return VG_ERR_INVALID_ARG;
+  const size_t o_bytes = rows_span(R, o_stride, width, 2);
+  if (rows_collide(q, q_stride, o, o_stride, R, width, width, 2) || kv8_overlaps(c, o, o_bytes)) return VG_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < kv8_attn_ws(c, rows, n_heads) || !aligned16(workspace))
+    return VG_ERR_WORKSPACE;
+  DevState* dev = nullptr;
+  if ((st = device_state(&dev)) != VG_OK) return st;
+  return kv8_attn_launch(c, rows, n_heads, q, q_stride, lens, first, n_new, scale, o, o_stride, workspace,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+struct AttnKv8Ws {
+  size_t pk, qkv, o, attn, total;
+};
+AttnKv8Ws attn_kv8_layout(const vg_kv8* c, int K) {
+  AttnKv8Ws L{};
+  const size_t R = (size_t)c->B * (K + 1);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  L.attn = take(kv8_attn_ws(c, K + 1, vg::kAttnHeads));
+  L.pk = take((size_t)kProjSplits * R * 3 * kH * 4);
+  L.qkv = take(R * 3 * kH * 2);
+  L.o = take(R * kH * 2);
+  L.total = off;
+  return L;
+}
+
+vg_status attn_kv8_check(const vg_kv8* c, int32_t K) {
+  if (K < 0 || K + 1 > vg::kAttnMaxRows) return VG_ERR_INVALID_ARG;
+  const vg_status st = kv8_attn_check(c, K + 1, c && c->n_kv > 0 ? c->n_kv : 1);
+  if (st != VG_OK) return st;
+  if (c->n_kv != vg::kAttnHeads || c->dim != vg::kAttnDim || c->L_max > 32768) return VG_ERR_UNSUPPORTED;
+  if ((int64_t)c->B * (K + 1) * kH >= ((int64_t)1 << 31)) return VG_ERR_UNSUPPORTED;
+  return VG_OK;
+}
+}  // namespace
+
+extern "C" size_t vg_attn_verify_kv8_workspace_bytes(const vg_kv8* c, int32_t K) {
+  if (attn_kv8_check(c, K) != VG_OK) return 0;
+  return attn_kv8_layout(c, K).total;
+}
+
+extern "C" vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* x, const void* w_qkv, const void* w_o,
+                                        const int32_t* lens, void* out, void* o_out, void* workspace,
+                                        size_t workspace_bytes, vg_stream_t stream) {
+  using namespace vg;
+  vg_status st = attn_kv8_check(c, K);
+  if (st != VG_OK) return st;
+  if (c->B == 0) return VG_OK;
+  if (!x || !w_qkv || !w_o || !lens || !out) return VG_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_qkv) || !aligned16(w_o) || !aligned16(out) || !aligned16(o_out) || !aligned4(lens))
+    return VG_ERR_INVALID_ARG;
+  const int R = c->B * (K + 1);
+  const size_t rows_bytes = (size_t)R * kH * 2;
+  if (overlaps(x, rows_bytes, out, rows_bytes) || kv8_overlaps(c, out, rows_bytes)) return VG_ERR_INVALID_ARG;
+  if (o_out && (overlaps(x, rows_bytes, o_out, rows_bytes) || overlaps(out, rows_bytes, o_out, rows_bytes) ||
+                kv8_overlaps(c, o_out, rows_bytes)))
+    return VG_ERR_INVALID_ARG;
+  const AttnKv8Ws L = attn_kv8_layout(c, K);
+  if (workspace == nullptr || workspace_bytes < L.total || !aligned16(workspace)) return VG_ERR_WORKSPACE;
+  DevState* dev = nullptr;
+  if ((st = device_state(&dev)) != VG_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* pk = reinterpret_cast<float*>(ws + L.pk);
+  __nv_bfloat16* qkv = reinterpret_cast<__nv_bfloat16*>(ws + L.qkv);
+  void* o = o_out ? o_out : ws + L.o;
+  if (attn_project(x, w_qkv, R, 3 * kH, pk, s) != cudaSuccess) return cuda_fail();
+  AttnArgs a{};
+  a.B = c->B;
+  a.K1 = K + 1;
+  a.L_max = c->L_max;
+  a.lens = lens;
+  a.qkv_part = pk;
+  a.splits = kProjSplits;
+  a.q = qkv;
+  if (launch_dep(attn_rope_append<true>, cdiv(R * kH / 2, 256), 256, 0, s, Launch::kPlain, a) != cudaSuccess)
+    return cuda_fail();
+  if ((st = kv8_append_launch(c, K + 1, qkv + kH, 3 * kH, qkv + 2 * kH, 3 * kH, lens, nullptr, s)) != VG_OK) return st;
+  if ((st = kv8_attn_launch(c, K + 1, kAttnHeads, qkv, 3 * kH, lens, nullptr, nullptr, 1.0f / sqrtf((float)kAttnDim), o,
+                            kH, ws + L.attn, s)) != VG_OK)
+    return st;
+  if (attn_project(o, w_o, R, kH, pk, s) != cudaSuccess) return cuda_fail();
+  if (launch_dep(attn_residual, cdiv(R * kH / 4, 256), 256, 0, s, Launch::kPlain, static_cast<const __nv_bfloat16*>(x),
+                 (const float*)pk, kProjSplits, R * kH, static_cast<__nv_bfloat16*>(out)) != cudaSuccess)
+    return cuda_fail();
+  return VG_OK;
+}
+
+// ------------------------------------------------------------ log probabilities
+namespace {
+
+// How a call is cut: vocabulary tile, tiles per unit of work, candidates per unit.
+struct LpPlan {
+  int tile_n, stages, n_vblk, group_tiles, n_groups, n_mblk, n_cand;
+  size_t stat, cand, total;
+};
+LpPlan lp_plan(int R, int V, int n_top) {
+  using namespace vg;
+  LpPlan p{};
+  p.n_cand = n_top > 0 ? n_top + kLpSpare : 0;
+  p.tile_n = 176;
+  p.stages = 5;
+  p.n_mblk = cdiv(R, kLpM);
+  p.n_vblk = cdiv(V, p.tile_n);
+  p.group_tiles = 5;
+  p.n_groups = cdiv(p.n_vblk, p.group_tiles);
+  p.stat = 0;
+  p.cand = align256((size_t)p.n_groups * 3 * R * 4);
+  p.total = p.cand + align256((size_t)p.n_groups * R * p.n_cand * 8);
+  return p;
+}
+
+vg_status lp_check(int32_t R, int32_t H, int32_t V, int32_t n_top) {
+  if (R < 0 || H < 1 || V < 1 || n_top < 0 || n_top > V) return VG_ERR_INVALID_ARG;
+  if (H % 64 != 0 || H > 8192 || n_top > vg::kLpMaxTop || R >= (1 << 24)) return VG_ERR_UNSUPPORTED;
+  return VG_OK;
+}
+
+}  // namespace
+
+extern "C" size_t vg_token_logprobs_workspace_bytes(int32_t R, int32_t H, int32_t V, int32_t n_top) {
+  if (lp_check(R, H, V, n_top) != VG_OK) return 0;
+  return lp_plan(R > 0 ? R : 1, V, n_top).total;
+}
+
+extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const void* h, const void* lm_head,
+                                       const int32_t* tokens, int32_t n_top, float* logprob, float* entropy,
+                                       int32_t* top_ids, float* top_logprobs, void* workspace, size_t workspace_bytes,
+                                       vg_stream_t stream) {
+  using namespace vg;
+  vg_status st = lp_check(R, H, V, n_top);
+  if (st != VG_OK) return st;
+  if (R == 0) return VG_OK;
+  if (!h || !lm_head || !aligned16(h) || !aligned16(lm_head) || !aligned4(tokens) || !aligned4(logprob) ||
+      !aligned4(entropy) || !aligned4(top_ids) || !aligned4(top_logprobs))
+    return VG_ERR_INVALID_ARG;
+  if ((logprob && !tokens) || (n_top > 0 && (!top_ids || !top_logprobs))) return VG_ERR_INVALID_ARG;
+  const LpPlan p = lp_plan(R, V, n_top);
+  if (workspace == nullptr || workspace_bytes < p.total || !aligned16(workspace)) return VG_ERR_WORKSPACE;
+  DevState* dev = nullptr;
+  if ((st = device_state(&dev)) != VG_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  LpArgs a{};
+  a.R = R;
+  a.V = V;
+  a.k_chunks = H / kBK;
+  a.n_mblk = p.n_mblk;
+  a.n_vblk = p.n_vblk;
+  a.group_tiles = p.group_tiles;
+  a.n_groups = p.n_groups;
+  a.a_box_rows = box_rows(R, kLpM);
+  a.b_box_rows = box_rows(V, p.tile_n);
+  a.tile_n = p.tile_n;
+  a.stages = p.stages;
+  a.n_cand = p.n_cand;
+  a.stat = reinterpret_cast<float*>(ws + p.stat);
+  a.cand = reinterpret_cast<unsigned long long*>(ws + p.cand);
+  CUtensorMap mH, mLM;
+  const uint64_t dH[2] = {(uint64_t)H, (uint64_t)R}, dL[2] = {(uint64_t)H, (uint64_t)V}, sK[1] = {(uint64_t)H * 2};
+  const uint32_t bH[2] = {kBK, (uint32_t)a.a_box_rows}, bL[2] = {kBK, (uint32_t)a.b_box_rows};
+  if (make_map(&mH, h, 2, dH, sK, bH) || make_map(&mLM, lm_head, 2, dL, sK, bL)) return VG_ERR_CUDA;
+  {
+    ProfScope ps(VG_KERNEL_LM_HEAD, s);
+    if (launch_dep(logprob_tiles, min(dev->sms, p.n_mblk * p.n_groups), 192, lp_smem_bytes(p.tile_n, p.stages, p.n_cand), s,
+                   Launch::kPlain, mH, mLM, a) != cudaSuccess)
+      return cuda_fail();
+  }
+  LpFinishArgs f{};
+  f.R = R;
+  f.H = H;
+  f.V = V;
+  f.n_groups = p.n_groups;
+  f.n_cand = p.n_cand;
+  f.n_top = n_top;
+  f.stat = a.stat;
+  f.cand = a.cand;
+  f.h = static_cast<const __nv_bfloat16*>(h);
+  f.lm = static_cast<const __nv_bfloat16*>(lm_head);
+  f.tokens = tokens;
+  f.logprob = logprob;
+  f.entropy = entropy;
+  f.top_ids = top_ids;
+  f.top_logprobs = top_logprobs;
+  if (launch_dep(logprob_finish, R, kLpFinishThreads, 0, s, Launch::kPlain, f) != cudaSuccess) return cuda_fail();
   return VG_OK;
 }
 

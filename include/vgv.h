@@ -411,6 +411,139 @@ vg_status vg_attn_verify(int32_t B, int32_t K, int32_t L_max, const void* x, con
                          size_t workspace_bytes, vg_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * KV cache in 8 bits, with one magnitude per block of positions and head. The
+ * pages give the position limit the cache has to hold (32,768; jina-ocr-v1
+ * model card, architecture paragraph) and no cache format; the format is this
+ * library's own. A code c stands for c * a / Q:
+ *   Q = 127, c an int8 in [-127, 127]           (VG_KV8_INT8)
+ *   Q = 448, c an e4m3 value                     (VG_KV8_E4M3)
+ *   a = the largest magnitude of the block's positions in that head, kept as an
+ *       fp32 that holds a bf16 value (0 for a block of zeros).
+ * Keys and values have magnitudes of their own. Inside a (sequence, head) the
+ * codes lie in groups of 16 positions, 16 * dim bytes each, in the order in
+ * which the attention's tensor-core fragments take them:
+ *   key   of position p, dimension d: byte [p / 16][d / 64][p % 16][d % 64]
+ *   value of position p, dimension d: byte [p / 16][d / 4][p % 16 / 4][d % 4][p % 4]
+ * Positions that were never written may hold any bytes.
+ * ------------------------------------------------------------------------- */
+#define VG_KV8_INT8 0
+#define VG_KV8_E4M3 1
+
+/* Element types of an output. */
+#define VG_BF16 0
+#define VG_F32 1
+
+typedef struct vg_kv8 {
+  int32_t format; /* VG_KV8_INT8 or VG_KV8_E4M3 */
+  int32_t B;      /* sequences */
+  int32_t L_max;  /* positions per sequence, a multiple of block, at most 2^20 */
+  int32_t n_kv;   /* key/value heads, 1 .. 1024 */
+  int32_t dim;    /* 64 or 128 */
+  int32_t block;  /* positions per magnitude: 16, 32, 64 or 128 */
+  void* k;        /* codes, B * n_kv * L_max * dim bytes each, 16-byte aligned */
+  void* v;
+  float* k_amax;  /* [B, n_kv, L_max / block] */
+  float* v_amax;
+} vg_kv8;
+
+/* Quantises new rows into the cache. k and v: bf16 rows of n_kv * dim elements,
+ * `rows` per sequence; row i < n_new[b] (n_new NULL: every row) of sequence b is
+ * row b * rows + i, k_stride (v_stride) elements after the row before it, and
+ * goes to position pos[b] + i. Rows behind n_new[b] are not read.
+ * A block whose first position is written takes the largest magnitude a of its
+ * new rows. One that already holds earlier positions (below pos[b]) keeps its
+ * magnitude, or takes a larger one where the new rows need it; then its earlier
+ * codes are rounded again: c' = round(c * a_old / a_new). New codes are
+ * round(x * Q / a). Every rounding is to nearest, ties to even, of the exact
+ * quotient. So a decode step that rewrites the positions of rejected drafts
+ * leaves a block's magnitude at least as large as those drafts needed.
+ * A NaN is stored as 0 and an infinity as the largest code of its sign, neither
+ * counts for the magnitude, and VG_ERR_DEVICE_BOUNDS is recorded. pos[b] < 0,
+ * n_new[b] outside [0, rows] or pos[b] + n_new[b] > L_max records
+ * VG_ERR_DEVICE_BOUNDS and leaves that sequence as it was. k and v 16-byte
+ * aligned, strides a multiple of 8 and at least n_kv * dim; neither may overlap
+ * the cache. One launch. Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED,
+ * VG_ERR_CUDA. */
+vg_status vg_kv8_append(const vg_kv8* c, int32_t rows, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, const int32_t* pos, const int32_t* n_new, vg_stream_t stream);
+
+/* Reads positions pos[b] .. pos[b] + n_rows[b] - 1 (n_rows NULL: rows) of every
+ * sequence back as values, rounded to out_type (VG_BF16 or VG_F32; fp32 values
+ * carry two fp32 roundings): position pos[b] + i becomes row b * rows + i of
+ * k_out and v_out (either may be NULL), laid out as in vg_kv8_append. Rows behind
+ * n_rows[b] are left as they were. Bad positions or counts record
+ * VG_ERR_DEVICE_BOUNDS and leave the sequence's rows as they were. One launch.
+ * Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED, VG_ERR_CUDA. */
+vg_status vg_kv8_read(const vg_kv8* c, int32_t rows, const int32_t* pos, const int32_t* n_rows, int32_t out_type,
+                      void* k_out, int64_t k_stride, void* v_out, int64_t v_stride, vg_stream_t stream);
+
+/* Attention of `rows` (1 .. 8) new query rows per sequence over the cache:
+ *   row i of sequence b sits at position lens[b] + i and sees positions
+ *   first[b] .. lens[b] + i (first NULL: 0); its own key and value are in the
+ *   cache already (vg_kv8_append). o = softmax(scale * q . k) v over them; a row
+ *   that sees nothing (first[b] > lens[b] + i) gets 0.
+ * q and o: bf16 rows of n_heads * dim elements, row b * rows + i, q_stride
+ * (o_stride) elements apart; query head h reads key/value head
+ * h / (n_heads / n_kv), at most 16 to a head. Rows i >= n_new[b] (n_new NULL:
+ * none) are not read and get o = 0. lens[b] < 0, first[b] < 0, n_new[b] outside
+ * [0, rows] or lens[b] + n_new[b] > L_max records VG_ERR_DEVICE_BOUNDS and gives
+ * o = 0 for that sequence. scale > 0.
+ * Precision: codes enter both products exactly (f16 operands, fp32 sums), query
+ * rows exactly down to 2^-29 of their largest element, softmax weights rounded
+ * to 2^-12 of themselves; sums and maxima are fp32, o is rounded once.
+ * workspace: vg_kv8_attn_workspace_bytes(c, rows, n_heads) bytes, 16-byte
+ * aligned. Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED (rows > 8, more than
+ * 16 query heads to a key/value head), VG_ERR_WORKSPACE, VG_ERR_CUDA. */
+size_t vg_kv8_attn_workspace_bytes(const vg_kv8* c, int32_t rows, int32_t n_heads);
+vg_status vg_kv8_attn(const vg_kv8* c, int32_t rows, int32_t n_heads, const void* q, int64_t q_stride,
+                      const int32_t* lens, const int32_t* first, const int32_t* n_new, float scale, void* o,
+                      int64_t o_stride, void* workspace, size_t workspace_bytes, vg_stream_t stream);
+
+/* vg_attn_verify on an 8-bit cache (n_kv = 10, dim = 128, L_max <= 32768; B is
+ * the cache's): the same layer, with the new rows' k (rotated) and v quantised
+ * into the cache (vg_kv8_append at positions lens[b] ..) and the rows' attention
+ * read from it (vg_kv8_attn, scale 1/sqrt(128)). Arguments and errors otherwise
+ * as there; unlike there, an overflowing sequence's two device errors share the
+ * status word. */
+size_t vg_attn_verify_kv8_workspace_bytes(const vg_kv8* c, int32_t K);
+vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* x, const void* w_qkv, const void* w_o,
+                             const int32_t* lens, void* out, void* o_out, void* workspace, size_t workspace_bytes,
+                             vg_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Log probabilities from the LM head, beside the greedy verification
+ * (vg_verify_greedy) of the same rows: for what was committed or drafted, how
+ * likely the model found it, how undecided it was, and its alternatives. The
+ * pages have no counterpart.
+ *   z[r,v]     = sum_h h[r,h] * lm_head[v,h],  lse[r] = log sum_v exp(z[r,v])
+ *   logprob[r] = z[r, tokens[r]] - lse[r]
+ *   entropy[r] = lse[r] - sum_v exp(z[r,v] - lse[r]) z[r,v]        (nats)
+ *   top_ids[r, 0 .. n_top-1]      = the n_top largest z[r,v], equal ones by lower v
+ *   top_logprobs[r, j]            = z[r, top_ids[r,j]] - lse[r]
+ * The logits are never stored. lse and the entropy come from tensor-core logits
+ * (fp32 sums); the given tokens' and the alternatives' logits are recomputed as
+ * exact products summed in fp64, so the order of close alternatives is that of
+ * the exact logits (an alternative can be missed only if more than four others
+ * lie within fp32 rounding of the n_top-th).
+ *   h        bf16 [R, H], H a multiple of 64, at most 8192
+ *   lm_head  bf16 [V, H]
+ *   tokens   int32 [R], or NULL if logprob is NULL. A negative token (the padding
+ *            of out_tokens) stands for none: its logprob is -inf. One >= V gives
+ *            -inf and records VG_ERR_DEVICE_BOUNDS.
+ *   logprob, entropy  fp32 [R], each may be NULL
+ *   top_ids, top_logprobs  int32 and fp32 [R, n_top], n_top 0 .. 20, at most V
+ * NaN logits make the row's log probabilities and entropy NaN and take no place
+ * among the alternatives; where fewer than n_top logits are above -inf the rest
+ * have id -1. R = 0 is a no-op. Two launches; workspace:
+ * vg_token_logprobs_workspace_bytes(R, H, V, n_top) bytes, 16-byte aligned.
+ * Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED, VG_ERR_WORKSPACE, VG_ERR_CUDA.
+ * ------------------------------------------------------------------------- */
+size_t vg_token_logprobs_workspace_bytes(int32_t R, int32_t H, int32_t V, int32_t n_top);
+vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const void* h, const void* lm_head, const int32_t* tokens,
+                            int32_t n_top, float* logprob, float* entropy, int32_t* top_ids, float* top_logprobs,
+                            void* workspace, size_t workspace_bytes, vg_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * The whole verify step for a handful of rows in ONE kernel launch: the
  * n_layers MoE layers (x_{l+1} = bf16(x_l + MoE_l(x_l)), as vg_moe_ffn_stack),
  * then the LM-head argmax and the prefix accept (as vg_verify_greedy). For

@@ -1,0 +1,216 @@
+"""Log probabilities from the LM head on the GPU against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+import greedy_speculative_verify_b200 as vgv
+import oracle
+import synth_inputs as si
+from oracle import kv8
+
+from gpu_common import D as DIMS, Guarded, dev, ensure_lib
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_lib()
+    vgv.vg_get_device_status()
+
+
+def call(h, lm, tokens, n_top, status=0):
+    R, H = h.shape
+    V = lm.shape[0]
+    gd = Guarded()
+    lp, en = gd.empty((R,), torch.float32, fill=7.0), gd.empty((R,), torch.float32, fill=7.0)
+    ids = gd.empty((R, n_top), torch.int32, fill=-9) if n_top else None
+    tl = gd.empty((R, n_top), torch.float32, fill=7.0) if n_top else None
+    ws = gd.empty((vgv.vg_token_logprobs_workspace_bytes(R, H, V, n_top),), torch.uint8, fill=0)
+    vgv.vg_token_logprobs(h, lm, tokens, lp, en, ids, tl, ws)
+    torch.cuda.synchronize()
+    assert vgv.vg_get_device_status()[0] == status
+    gd.check()
+    n = lambda t: None if t is None else t.cpu().numpy()
+    return n(lp), n(en), n(ids), n(tl)
+
+
+def tolerances(lp, mag, H):
+    """What lse and the entropy may be off by: a logit is an fp32 sum of H exact
+    products, off by up to 6 sqrt(H) 2^-23 of the sum of their magnitudes (sums
+    whose roundings do not conspire stay within 6 standard deviations); lse moves
+    by at most the largest error, p-weighted; its sums of exponentials carry
+    fewer than 128 roundings in a row and 2^-21 each for the exponential. The
+    entropy is a p-weighted mean of log p, whose terms shift with p too."""
+    ez = 6 * np.sqrt(H) * 2.0 ** -23 * mag.max(axis=1)
+    p = np.exp(lp)
+    spread = (p * np.abs(lp)).sum(axis=1)
+    rel = 128 * 2.0 ** -24 + 2.0 ** -21
+    return ez + rel + 2.0 ** -23 * np.abs(lp).max(axis=1), (2 * ez + 2 * rel) * (1 + spread) + 2.0 ** -22 * spread
+
+
+def check(h, lm, tokens, n_top):
+    """h, lm: bf16 bits."""
+    R, H = h.shape
+    lp, ent, mag = kv8.logprobs(h, lm)
+    t_lse, t_ent = tolerances(lp, mag, H)
+    got_lp, got_en, ids, tl = call(dev(h), dev(lm), torch.from_numpy(tokens).cuda(), n_top)
+    want = np.where(tokens >= 0, lp[np.arange(R), np.maximum(tokens, 0)], -np.inf)
+    real = tokens >= 0
+    assert (np.abs(got_lp[real] - want[real]) <= t_lse[real] + 2.0 ** -24 * np.abs(want[real])).all()
+    assert (got_lp[~real] == -np.inf).all()
+    assert (np.abs(got_en - ent) <= t_ent).all(), float((np.abs(got_en - ent) / t_ent).max())
+    if n_top:
+        order = np.lexsort((np.broadcast_to(np.arange(lm.shape[0]), lp.shape), -lp), axis=1)[:, :n_top]
+        # logits of equal rows are equal, and fp64 sums in another order may differ in the last place
+        z = np.take_along_axis(lp, order, 1)
+        same = np.take_along_axis(lp, ids.astype(np.int64), 1)
+        assert (np.abs(same - z) <= 1e-12 * np.abs(mag).max()).all()
+        gap = np.diff(lp[np.arange(R)[:, None], order], axis=1)
+        clear = np.ones_like(order, bool)
+        clear[:, 1:] &= np.abs(gap) > 1e-11
+        clear[:, :-1] &= np.abs(gap) > 1e-11
+        clear[:, -1] = False  # its follower is not in the list
+        assert np.array_equal(ids[clear], order[clear])
+        assert (np.abs(tl - z) <= t_lse[:, None] + 2.0 ** -24 * np.abs(z)).all()
+
+
+def inputs(R, H, V, seed, sure=0.0):
+    g = np.random.default_rng(seed)
+    lm = oracle.round_bf16_bits(g.normal(0, 1.2 / np.sqrt(H), (V, H)))
+    tok = g.integers(0, V, R).astype(np.int32)
+    x = g.normal(0, 1, (R, H)) + sure * g.uniform(0, 1, (R, 1)) * oracle.widen(lm[tok])
+    return oracle.round_bf16_bits(x), lm, tok
+
+
+@pytest.mark.parametrize("R,H,V,n_top", [
+    (1, 64, 1, 1), (1, 64, 20, 20), (3, 128, 7, 0), (5, 256, 175, 5), (127, 64, 177, 3), (128, 128, 1000, 20),
+    (129, 320, 881, 7), (300, 64, 1761, 1), (257, 1280, 4099, 20), (4, 2048, 999, 12), (2, 8192, 333, 2)])
+def test_logprobs(R, H, V, n_top):
+    h, lm, tok = inputs(R, H, V, seed=R + V, sure=8.0)
+    tok[::4] = -1
+    check(h, lm, tok, n_top)
+
+
+def test_full_vocabulary():
+    h, lm, tok = inputs(8, DIMS.H, DIMS.V, seed=5, sure=14.0)
+    check(h, lm, tok, 20)
+
+
+def test_many_row_blocks():
+    """4,096 rows in 32 row blocks over a vocabulary of many groups: the rows
+    repeat eight, so every block has to give the same answers."""
+    h, lm, tok = inputs(8, 256, 20011, seed=6, sure=10.0)
+    rep = lambda a: np.tile(a, (512,) + (1,) * (a.ndim - 1))
+    few = call(dev(h), dev(lm), torch.from_numpy(tok).cuda(), 5)
+    many = call(dev(rep(h)), dev(lm), torch.from_numpy(rep(tok)).cuda(), 5)
+    check(h, lm, tok, 5)
+    for a, b in zip(few[2:3], many[2:3]):
+        assert np.array_equal(rep(a), b)
+    for a, b in zip((few[0], few[1], few[3]), (many[0], many[1], many[3])):
+        # only the grouping of the sums differs with the number of rows
+        assert np.allclose(rep(a), b, rtol=1e-5, atol=1e-5)
+        assert np.array_equal(np.tile(b[:8], (512,) + (1,) * (b.ndim - 1)), b)
+
+
+def test_rising_logits():
+    """Logits that rise with the vocabulary index: every column enters the list
+    of alternatives, the worst order for it; and falling, and all equal."""
+    V, H = 3001, 64
+    base = np.zeros((V, H))
+    base[:, 0] = np.arange(V) // 8 * 8.0  # exact in bf16 up to 2^11 in steps of 8
+    lm = oracle.round_bf16_bits(base)
+    h = np.zeros((3, H))
+    h[:, 0] = [2.0 ** -7, -(2.0 ** -7), 0.0]
+    tok = np.array([3000, 0, 17], np.int32)
+    lp, _, _ = kv8.logprobs(oracle.round_bf16_bits(h), lm)
+    _, _, ids, _ = call(dev(oracle.round_bf16_bits(h)), dev(lm), torch.from_numpy(tok).cuda(), 20)
+    order = np.lexsort((np.broadcast_to(np.arange(V), lp.shape), -lp), axis=1)[:, :20]
+    assert np.array_equal(ids, order)  # ties to the lower index
+
+
+def test_order_of_alternatives_closer_than_fp32():
+    """Two tokens whose logits differ by less than an fp32 sum resolves, in both
+    index orders: the larger exact logit comes first."""
+    H, V = 64, 400
+    lm = np.zeros((V, H))
+    lm[:, 0] = -1.0
+    lm[[50, 300], 0] = 256.0
+    lm[300, 1] = 2.0 ** -12
+    lm[[120, 121], 0] = 128.0
+    lm[120, 1] = 2.0 ** -12
+    h = np.zeros((1, H))
+    h[0, :2] = [256.0, 2.0 ** -4]  # 65,536 against 65,536 + 2^-16, below half an ulp
+    _, _, ids, _ = call(dev(oracle.round_bf16_bits(h)), dev(oracle.round_bf16_bits(lm)), torch.tensor([5], dtype=torch.int32).cuda(), 4)
+    assert ids[0].tolist() == [300, 50, 120, 121]
+
+
+def test_nan_and_infinite_logits_and_bad_tokens():
+    g = np.random.default_rng(8)
+    h, lm, tok = inputs(6, 128, 500, seed=8)
+    hb, lb = h.copy(), lm.copy()
+    hb[1, 3] = 0x7FC0  # a NaN row
+    hb[2, 0] = 0x7F7F  # with 3e38: overflows against the row below
+    lb[40, :] = 0
+    lb[40, 0] = 0xFF7F  # -3.4e38: logit -inf in row 2, hugely negative elsewhere
+    tok[3], tok[4], tok[5] = 500, -1, 499
+    lp, en, ids, tl = call(dev(hb), dev(lb), torch.from_numpy(tok).cuda(), 3, status=6)
+    assert np.isnan(lp[1]) and np.isnan(en[1]) and (ids[1] == -1).all()
+    assert lp[3] == -np.inf and lp[4] == -np.inf and np.isfinite(lp[5])
+    ref, ent, _ = kv8.logprobs(hb[[0, 5]], lb)
+    assert np.allclose(lp[[0, 5]], ref[[0, 1], tok[[0, 5]]], atol=1e-3) and np.allclose(en[[0, 5]], ent, atol=1e-3)
+
+
+def test_only_what_is_asked_for():
+    h, lm, tok = inputs(9, 128, 640, seed=10)
+    hd, ld, td = dev(h), dev(lm), torch.from_numpy(tok).cuda()
+    full = call(hd, ld, td, 4)
+    ws = torch.zeros(vgv.vg_token_logprobs_workspace_bytes(9, 128, 640, 4), dtype=torch.uint8, device="cuda")
+    en = torch.zeros(9, device="cuda")
+    vgv.vg_token_logprobs(hd, ld, None, None, en, None, None, ws)
+    lp = torch.zeros(9, device="cuda")
+    vgv.vg_token_logprobs(hd, ld, td, lp, None, None, None, ws)
+    torch.cuda.synchronize()
+    assert np.array_equal(en.cpu().numpy(), full[1]) and np.array_equal(lp.cpu().numpy(), full[0])
+    assert vgv.vg_get_device_status()[0] == 0
+
+
+def test_verify_step_with_logprobs():
+    """A run as a server makes it: attention on the 8-bit cache, the LM head's
+    verification, the log probabilities of what was committed; the committed
+    tokens are the first alternatives of their rows."""
+    H, V, B, K, L = DIMS.H, 8191, 4, 3, 256
+    g = np.random.default_rng(12)
+    wqkv, wo = (dev(oracle.round_bf16_bits(g.normal(0, s, (n, H)))) for s, n in ((0.02, 3 * H), (0.05, H)))
+    lm = dev(oracle.round_bf16_bits(g.normal(0, 1.2 / np.sqrt(H), (V, H))))
+    t = [torch.zeros(B, 10, L, 128, dtype=torch.int8, device="cuda") for _ in "kv"]
+    a = [torch.zeros(B, 10, L // 64, device="cuda") for _ in "kv"]
+    cache = vgv.make_kv8(*t, *a)
+    lens = torch.tensor([0, 5, 63, 200], dtype=torch.int32, device="cuda")
+    prompt = dev(oracle.round_bf16_bits(g.normal(0, 1, (B * 200, 2 * H))))
+    vgv.vg_kv8_append(cache, 200, prompt[:, :H], prompt[:, H:], torch.zeros_like(lens), n_new=lens)
+    z8 = lambda n: torch.zeros(n, dtype=torch.uint8, device="cuda")
+    ws_a = z8(vgv.vg_attn_verify_kv8_workspace_bytes(cache, K))
+    ws_v = z8(vgv.vg_verify_workspace_bytes(B, K, H, V))
+    R = B * (K + 1)
+    ws_l = z8(vgv.vg_token_logprobs_workspace_bytes(R, H, V, 2))
+    out = torch.empty(R, H, dtype=torch.bfloat16, device="cuda")
+    am, acc = torch.empty(R, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    tok = torch.empty(B, K + 1, dtype=torch.int32, device="cuda")
+    lp, en = torch.empty(R, device="cuda"), torch.empty(R, device="cuda")
+    ids, tl = torch.empty(R, 2, dtype=torch.int32, device="cuda"), torch.empty(R, 2, device="cuda")
+    for step in range(3):
+        x = dev(oracle.round_bf16_bits(g.normal(0, 1, (R, H))))
+        drafts = torch.from_numpy(g.integers(0, V, (B, K)).astype(np.int32)).cuda()
+        if step:
+            drafts[:, 0] = am.view(B, K + 1)[:, 0]
+        vgv.vg_attn_verify_kv8(cache, K, x, wqkv, wo, lens, out, ws_a)
+        vgv.vg_verify_greedy(B, K, H, V, out, lm, drafts, am, acc, tok, ws_v)
+        vgv.vg_token_logprobs(out, lm, tok.view(-1), lp, en, ids, tl, ws_l)
+        lens += acc + 1
+        torch.cuda.synchronize()
+        assert vgv.vg_get_device_status()[0] == 0
+        committed = tok.view(-1) >= 0
+        assert torch.equal(ids[committed, 0], tok.view(-1)[committed])
+        assert torch.equal(lp[committed], tl[committed, 0])
+        assert bool((lp[~committed] == -torch.inf).all()) and bool((tl[:, 0] >= tl[:, 1]).all()) and bool((en > 0).all())
