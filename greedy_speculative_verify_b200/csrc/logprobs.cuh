@@ -8,13 +8,14 @@
 // rows as N; a unit of work is a group of consecutive vocabulary tiles for one
 // 128-row block. The epilogue thread that owns a row reads its logits from
 // tensor memory and keeps, in one pass, the running maximum m, S = sum e^(z-m),
-// T = sum e^(z-m) (z-m), and the candidates: the n + kLpSpare largest logits.
+// T = sum e^(z-m) (z-m), and the candidates: the largest logits, at least kLpSpare more than
+// the n asked for.
 // logprob_finish: one CTA per row joins the units' partials (S and T rescaled to
-// the common maximum), takes the n + kLpSpare best candidates of all units and
+// the common maximum), takes the best candidates of all units and
 // recomputes their logits and the given token's as sums of exact products in
 // fp64, so that the order of close alternatives is that of the exact dot
 // products and does not depend on the tensor cores' summation; kLpSpare
-// candidates beyond n keep one from being lost to fp32 rounding at the border.
+// or more candidates beyond n keep one from being lost to fp32 rounding at the border.
 #pragma once
 #include "common.cuh"
 #include "gemm_moe.cuh"
@@ -27,18 +28,25 @@ constexpr int kLpSpare = 4;
 constexpr int kLpM = 128;
 constexpr int kLpABytes = kLpM * kBK * 2;
 constexpr int kLpAux = 1024;
+constexpr int kLpChunk = 16;             // columns read from tensor memory at a time
+constexpr int kLpPend = 8 + kLpChunk;    // columns a row can have waiting for its candidate list
 
 struct LpArgs {
   int R, V, k_chunks, n_mblk, n_vblk, group_tiles, n_groups, a_box_rows, b_box_rows;
-  int tile_n, stages, n_cand;  // vocabulary rows per tile, pipeline stages, candidates kept per unit (0: none)
+  int tile_n, stages;          // vocabulary rows per tile, pipeline stages
   float* stat;                 // [n_groups][3][R]: m, S, T
-  unsigned long long* cand;    // [n_groups][R][n_cand]: order-preserving keys, descending; 0 = none
+  unsigned long long* cand;    // [n_groups][R][NC]: order-preserving keys, descending; 0 = none
+  uint32_t* floor;             // [R] or null: order-preserving image of a logit that NC others reach (0: none known)
 };
 
 __host__ __device__ constexpr int lp_stage_bytes(int tile_n) { return kLpABytes + tile_n * kBK * 2; }
-__host__ __device__ constexpr int lp_smem_bytes(int tile_n, int stages, int n_cand) {
-  return 1024 + stages * lp_stage_bytes(tile_n) + kLpAux + n_cand * kLpM * 8;
+__host__ __device__ constexpr int lp_smem_bytes(int tile_n, int stages) {
+  return 1024 + stages * lp_stage_bytes(tile_n) + kLpAux + kLpPend * kLpM * 8;
 }
+
+// Candidates kept for n alternatives: n + kLpSpare rounded up to a size the
+// kernels are built for.
+__host__ __device__ constexpr int lp_cands(int n_top) { return n_top <= 8 ? 12 : 24; }
 
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -46,6 +54,36 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// A row's best logits so far, descending (equal ones by index), in registers.
+template <int NC>
+struct LpList {
+  float z[NC];
+  int v[NC];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) z[k] = -INFINITY, v[k] = -1;
+  }
+  // Columns come in increasing order, so an equal logit goes behind.
+  __device__ __forceinline__ void insert(float x, int i) {
+    bool ahead[NC];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) ahead[k] = x > z[k];
+#pragma unroll
+    for (int k = NC - 1; k > 0; --k) {
+      z[k] = ahead[k] ? (ahead[k - 1] ? z[k - 1] : x) : z[k];
+      v[k] = ahead[k] ? (ahead[k - 1] ? v[k - 1] : i) : v[k];
+    }
+    z[0] = ahead[0] ? x : z[0];
+    v[0] = ahead[0] ? i : v[0];
+  }
+};
+
+// An fp32 logit's image in the order of argmax_key's high word, and back.
+__device__ __forceinline__ float lp_unkey(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
+}
+
+template <int NC>
 __global__ void __launch_bounds__(192, 1)
     logprob_tiles(const __grid_constant__ CUtensorMap mapH, const __grid_constant__ CUtensorMap mapLM, const LpArgs a) {
   constexpr int kMaxStages = 8;
@@ -60,7 +98,7 @@ __global__ void __launch_bounds__(192, 1)
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  unsigned long long* list = reinterpret_cast<unsigned long long*>(aux + kLpAux);  // [n_cand][kLpM]
+  float2* pend = reinterpret_cast<float2*>(aux + kLpAux);  // [kLpPend][kLpM]: (logit, column) waiting
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int total = a.n_groups * a.n_mblk;  // unit = (vocabulary group, row block), row block fastest
@@ -191,46 +229,68 @@ __global__ void __launch_bounds__(192, 1)
       mbar_wait(mma_done, 0, limit);
     }
   } else {
+    // Candidates: a logit above the list's last one is first parked in shared
+    // memory, and the parked ones of all 32 rows of the warp enter their lists
+    // together, so the insertion runs about as often as a row has insertions and
+    // not whenever any of 32 rows has one.
     const int q = warp & 3;
     const int row = q * 32 + lane;
-    const int nc = a.n_cand;
     int lt = 0;
     bool ok = true;
+    LpList<NC> list;
     for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
       const int g = u / a.n_mblk, mb = u - g * a.n_mblk;
       const int vb1 = min(a.n_vblk, (g + 1) * a.group_tiles);
       const int r = mb * kLpM + row;
+      const bool busy = mb * kLpM + q * 32 < a.R;  // this warp has rows
       float m = -INFINITY, S = 0.0f, T = 0.0f;
-      float worst = -INFINITY;  // the last candidate's logit: only larger ones enter
-      for (int k = 0; k < nc; ++k) list[k * kLpM + row] = 0ull;
-      for (int vb = g * a.group_tiles; vb < vb1; ++vb, ++lt) {
-        if (*abort_flag) {
-          ok = false;
-          break;
+      float least = -INFINITY;  // only larger logits enter
+      int parked = 0;
+      list.clear();
+      if (r >= a.R) {
+        least = INFINITY;  // nothing enters
+      } else if (a.floor) {
+        const uint32_t f = *reinterpret_cast<volatile uint32_t*>(a.floor + r);
+        // a logit equal to the floor still enters: step just below it (zero: below the image of -0 too)
+        if (f > 2u) least = lp_unkey(f == 0x80000000u ? f - 2u : f - 1u);
+      }
+      auto settle = [&]() {  // the parked columns into the list
+        const int most = __reduce_max_sync(0xffffffffu, parked);
+        for (int i = 0; i < most; ++i) {
+          const float2 p = pend[i * kLpM + row];
+          list.insert(i < parked ? p.x : -INFINITY, __float_as_int(p.y));
         }
+        parked = 0;
+        least = fmaxf(least, list.z[NC - 1]);
+      };
+      for (int vb = g * a.group_tiles; vb < vb1; ++vb, ++lt) {
         const int ab = lt & 1;
         const uint32_t ap = (lt >> 1) & 1;
-        if (!mbar_wait(&tfull[ab], ap, limit)) {
-          record_error(kErrTimeout, 354);
+        // one decision for the warp: the votes below need all its lanes
+        ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&tfull[ab], ap, limit));
+        if (!ok) {
+          if (!*abort_flag) record_error(kErrTimeout, 354);
           *abort_flag = 1;
-          ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t t0 = tmem_base + ((uint32_t)(q * 32) << 16) + ab * 256;
-        const int v0 = vb * a.tile_n;
+        const int v0 = vb * a.tile_n, cols = busy ? min(a.tile_n, a.V - v0) : 0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < a.tile_n; c0 += 16) {
-          if (v0 + c0 >= a.V) break;
-          uint32_t zb[16];
+        for (int c0 = 0; c0 < cols; c0 += kLpChunk) {
+          uint32_t zb[kLpChunk];
           tmem_ld16(t0 + c0, zb);
           tmem_ld_wait();
-          float z[16], top = -INFINITY;
+          float z[kLpChunk], top = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            z[j] = v0 + c0 + j < a.V ? __uint_as_float(zb[j]) : -INFINITY;
-            top = fmaxf(top, z[j]);
+          for (int j = 0; j < kLpChunk; ++j) z[j] = __uint_as_float(zb[j]);
+          if (c0 + kLpChunk > cols) {  // behind the vocabulary
+#pragma unroll
+            for (int j = 0; j < kLpChunk; ++j)
+              if (c0 + j >= cols) z[j] = -INFINITY;
           }
+#pragma unroll
+          for (int j = 0; j < kLpChunk; ++j) top = fmaxf(top, z[j]);
           const float now = fmaxf(m, top), base = now > -INFINITY ? now : 0.0f;
           if (now > m && m > -INFINITY) {  // to the new maximum
             const float d = fmaxf(m - now, -1000.0f), f = ex2_approx(d * 1.4426950408889634f);
@@ -240,42 +300,38 @@ __global__ void __launch_bounds__(192, 1)
           m = now;
           float s1 = 0.0f, t1 = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
+          for (int j = 0; j < kLpChunk; ++j) {
             const float d = z[j] - base, e = ex2_approx(d * 1.4426950408889634f);
             s1 += e;
             t1 = fmaf(e, fmaxf(d, -1000.0f), t1);  // a weight of 0 adds 0, also where z is -inf
           }
           S += s1;
           T += t1;
-          if (nc > 0 && r < a.R && top > worst) {
-            for (int j = 0; j < 16; ++j) {
-              if (!(z[j] > worst)) continue;
-              unsigned long long key = argmax_key(z[j], (uint32_t)(v0 + c0 + j));
-              int k = nc - 1;
-              while (k > 0 && list[(k - 1) * kLpM + row] < key) {
-                list[k * kLpM + row] = list[(k - 1) * kLpM + row];
-                --k;
+          if (__any_sync(0xffffffffu, top > least)) {
+#pragma unroll
+            for (int j = 0; j < kLpChunk; ++j)
+              if (z[j] > least) {
+                pend[parked * kLpM + row] = make_float2(z[j], __int_as_float(v0 + c0 + j));
+                ++parked;
               }
-              list[k * kLpM + row] = key;
-              const unsigned long long w = list[(nc - 1) * kLpM + row];
-              if (w != 0ull) {
-                const uint32_t uw = (uint32_t)(w >> 32);
-                worst = __uint_as_float((uw & 0x80000000u) ? uw & 0x7FFFFFFFu : ~uw);
-              }
-            }
+            if (__any_sync(0xffffffffu, parked > kLpPend - kLpChunk)) settle();
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[ab]);
       }
+      if (busy) settle();
       if (ok && r < a.R) {
         float* st = a.stat + (size_t)g * 3 * a.R + r;
         st[0] = m;
         st[a.R] = S;
         st[2 * (size_t)a.R] = T;
-        unsigned long long* dst = a.cand + ((size_t)g * a.R + r) * nc;
-        for (int k = 0; k < nc; ++k) dst[k] = list[k * kLpM + row];
+        unsigned long long* dst = a.cand + ((size_t)g * a.R + r) * NC;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) dst[k] = list.v[k] >= 0 ? argmax_key(list.z[k], (uint32_t)list.v[k]) : 0ull;
+        if (a.floor && list.v[NC - 1] >= 0)
+          atomicMax(a.floor + r, (uint32_t)(argmax_key(list.z[NC - 1], 0u) >> 32));
       }
     }
   }
@@ -287,7 +343,7 @@ __global__ void __launch_bounds__(192, 1)
 }
 
 struct LpFinishArgs {
-  int R, H, V, n_groups, n_cand, n_top;
+  int R, H, V, n_groups, n_top;
   const float* stat;
   const unsigned long long* cand;
   const __nv_bfloat16* h;
@@ -299,20 +355,36 @@ struct LpFinishArgs {
   float* top_logprobs;    // [R, n_top]
 };
 
-constexpr int kLpFinishThreads = 128;
+constexpr int kLpFinishThreads = 256;
+constexpr int kLpMaxGroups = 512;
+constexpr int kLpFix = 12;  // candidates whose exact logits enter the sums: the same however many alternatives are asked for
 
-// One CTA per row.
+// One CTA per row. The best NC candidates of all units: the NC-th largest of the
+// units' first ones bounds them from below, so at most NC lists have any, and a
+// rank count orders what is left. Their tensor-core logits are replaced by the
+// exact ones in the sums too: the tensor cores cut every partial sum towards
+// zero (about 1.5e-8 of a logit for each 16 products, 1.2e-6 at H = 1,280), which
+// shifts all logits alike but for their size, so where a few tokens hold the
+// mass, correcting those removes most of the error.
+template <int NC>
 __global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinishArgs a) {
-  constexpr int NW = kLpFinishThreads / 32, kMost = kLpMaxTop + kLpSpare;
+  constexpr int NW = kLpFinishThreads / 32;
   __shared__ float red_m[NW];
-  __shared__ double red_s[NW], red_t[NW], z_s[kMost + 1];
-  __shared__ int id_s[kMost + 1];
+  __shared__ double red_s[NW], red_t[NW], z_s[NC + 1], s_fix[kLpFix], t_fix[kLpFix];
+  __shared__ unsigned long long head[kLpMaxGroups], pool[NC * NC], best[NC];
+  __shared__ unsigned long long floor_s;
+  __shared__ int id_s[NC + 1], n_pool;
   griddep_launch_dependents();
   griddep_wait();
   const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) n_pool = 0, floor_s = 1ull;  // 0 keys are no candidates
+  if (tid < NC) best[tid] = 0ull;
   // ---- the units' sums, rescaled to the common maximum
   float m = -INFINITY;
-  for (int g = tid; g < a.n_groups; g += kLpFinishThreads) m = fmaxf(m, a.stat[(size_t)g * 3 * a.R + r]);
+  for (int g = tid; g < a.n_groups; g += kLpFinishThreads) {
+    m = fmaxf(m, a.stat[(size_t)g * 3 * a.R + r]);
+    head[g] = a.cand[((size_t)g * a.R + r) * NC];
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red_m[warp] = m;
@@ -325,6 +397,10 @@ __global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinis
     const double d = mg > -INFINITY ? (double)mg - (double)m : 0.0, f = mg > -INFINITY ? exp(d) : 1.0;
     S += f * Sg;
     T += f * (Tg + Sg * d);
+    int rank = 0;
+    const unsigned long long mine = head[g];
+    for (int k = 0; k < a.n_groups; ++k) rank += head[k] > mine;
+    if (rank == NC - 1 && mine) floor_s = mine;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -332,79 +408,87 @@ __global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinis
     T += __shfl_xor_sync(0xffffffffu, T, o);
   }
   if (lane == 0) red_s[warp] = S, red_t[warp] = T;
-  // ---- the best candidates of all units: one warp, each lane walking the lists g = lane, lane + 32, ...
-  if (warp == 0 && a.n_cand > 0) {
-    for (int k = 0; k < a.n_cand; ++k) {
-      // the k-th best key is the largest below the previous one
-      const unsigned long long below = k == 0 ? ~0ull : ((unsigned long long)__double_as_longlong(z_s[k - 1]));
-      unsigned long long best = 0ull;
-      for (int g = lane; g < a.n_groups; g += 32) {
-        const unsigned long long* l = a.cand + ((size_t)g * a.R + r) * a.n_cand;
-        for (int i = 0; i < a.n_cand; ++i) {
-          const unsigned long long key = l[i];
-          if (key < below) {
-            best = key > best ? key : best;
-            break;
-          }
-        }
+  __syncthreads();
+  for (int g = tid; g < a.n_groups; g += kLpFinishThreads)
+    if (head[g] >= floor_s) {
+      const unsigned long long* l = a.cand + ((size_t)g * a.R + r) * NC;
+#pragma unroll 4
+      for (int k = 0; k < NC; ++k) {
+        const unsigned long long key = l[k];
+        if (key < floor_s) break;
+        pool[atomicAdd(&n_pool, 1)] = key;
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
-        best = other > best ? other : best;
-      }
-      if (lane == 0) {
-        z_s[k] = __longlong_as_double((long long)best);  // the key itself, until the logits replace it
-        id_s[k] = best ? (int)(0xFFFFFFFFu - (uint32_t)(best & 0xFFFFFFFFull)) : -1;
-      }
-      __syncwarp();
     }
+  __syncthreads();
+  for (int i = tid; i < n_pool; i += kLpFinishThreads) {
+    const unsigned long long mine = pool[i];
+    int rank = 0;
+    for (int k = 0; k < n_pool; ++k) rank += pool[k] > mine;
+    if (rank < NC) best[rank] = mine;
   }
   const int tok = a.tokens ? a.tokens[r] : -1;
+  __syncthreads();
+  if (tid < NC) id_s[tid] = best[tid] ? (int)(0xFFFFFFFFu - (uint32_t)(best[tid] & 0xFFFFFFFFull)) : -1;
   if (tid == 0) {
-    id_s[a.n_cand] = tok >= 0 && tok < a.V ? tok : -1;
+    id_s[NC] = tok >= 0 && tok < a.V ? tok : -1;
     if (tok >= a.V) record_error(kErrBounds, 355);
   }
   __syncthreads();
   // ---- their logits from exact products (a product of two bf16 is exact in fp32), summed in fp64
-  for (int k = warp; k <= a.n_cand; k += NW) {
+  for (int k = warp; k <= NC; k += NW) {
     const int v = id_s[k];
     double z = -INFINITY;
     if (v >= 0) {
-      z = 0.0;
       const uint4* x = reinterpret_cast<const uint4*>(a.h + (size_t)r * a.H);
       const uint4* w = reinterpret_cast<const uint4*>(a.lm + (size_t)v * a.H);
+      double z0 = 0.0, z1 = 0.0, z2 = 0.0, z3 = 0.0;
+#pragma unroll 2
       for (int i = lane; i < a.H / 8; i += 32) {
         const uint4 xv = x[i], wv = w[i];
-        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w}, ws[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z += (double)(bf16_lo(xs[e]) * bf16_lo(ws[e]));
-          z += (double)(bf16_hi(xs[e]) * bf16_hi(ws[e]));
-        }
+        z0 += (double)(bf16_lo(xv.x) * bf16_lo(wv.x));
+        z1 += (double)(bf16_hi(xv.x) * bf16_hi(wv.x));
+        z2 += (double)(bf16_lo(xv.y) * bf16_lo(wv.y));
+        z3 += (double)(bf16_hi(xv.y) * bf16_hi(wv.y));
+        z0 += (double)(bf16_lo(xv.z) * bf16_lo(wv.z));
+        z1 += (double)(bf16_hi(xv.z) * bf16_hi(wv.z));
+        z2 += (double)(bf16_lo(xv.w) * bf16_lo(wv.w));
+        z3 += (double)(bf16_hi(xv.w) * bf16_hi(wv.w));
       }
+      z = (z0 + z1) + (z2 + z3);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     }
-    __syncwarp();
-    if (lane == 0) z_s[k] = z;
+    if (lane == 0) {
+      z_s[k] = z;
+      if (k < kLpFix) {  // what the exact logit changes in S and T
+        double ds = 0.0, dt = 0.0;
+        if (v >= 0 && m < INFINITY) {
+          const double d0 = (double)lp_unkey((uint32_t)(best[k] >> 32)) - (double)m, d1 = z - (double)m;
+          const double e0 = exp(d0), e1 = exp(d1);
+          ds = e1 - e0;
+          dt = e1 * d1 - e0 * d0;
+        }
+        s_fix[k] = ds, t_fix[k] = dt;
+      }
+    }
   }
   __syncthreads();
   S = 0.0, T = 0.0;
   for (int w = 0; w < NW; ++w) S += red_s[w], T += red_t[w];
+  for (int k = 0; k < kLpFix; ++k) S += s_fix[k], T += t_fix[k];
   const double log_s = log(S), lse = (double)m + log_s;
   if (tid == 0) {
-    if (a.logprob) a.logprob[r] = (float)(z_s[a.n_cand] - lse);
+    if (a.logprob) a.logprob[r] = (float)(z_s[NC] - lse);
     if (a.entropy) a.entropy[r] = (float)(log_s - T / S);
   }
   // ---- order: rank of each candidate by (logit, lower index first)
-  if (tid < a.n_cand) {
+  if (tid < NC) {
     const double z = z_s[tid];
     const int v = id_s[tid];
     int rank = 0;
-    for (int k = 0; k < a.n_cand; ++k) {
+    for (int k = 0; k < NC; ++k) {
       if (k == tid) continue;
-      // candidates that are missing (fewer finite logits than asked for) come last, in list order
+      // candidates that are missing (fewer logits above -inf than asked for) come last, in list order
       const bool ahead = id_s[k] < 0 ? (v < 0 && k < tid) : (v < 0 || z_s[k] > z || (z_s[k] == z && id_s[k] < v));
       rank += ahead;
     }

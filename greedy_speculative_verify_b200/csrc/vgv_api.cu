@@ -150,8 +150,11 @@ vg_status device_state(DevState** out) {
     if (cudaFuncSetAttribute(vg::lmhead_argmax_accept, cudaFuncAttributeMaxDynamicSharedMemorySize, vg::kLmSmemBytes) !=
         cudaSuccess)
       return cuda_fail();
-    if (cudaFuncSetAttribute(vg::logprob_tiles, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes) != cudaSuccess)
-      return cuda_fail();
+    for (auto* k : {vg::logprob_tiles<12>, vg::logprob_tiles<24>})
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes) != cudaSuccess ||
+          cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+              cudaSuccess)
+        return cuda_fail();
     // Kernels that follow each other with dependent launches share SMs only if
     // their shared-memory configurations agree: every kernel of the decode
     // chain asks for the largest shared-memory carveout.
@@ -167,7 +170,6 @@ vg_status device_state(DevState** out) {
           cudaFuncSetAttribute(vg::moe_combine<true>, kC, kMax) != cudaSuccess ||
           cudaFuncSetAttribute(vg::moe_combine<false>, kC, kMax) != cudaSuccess ||
           cudaFuncSetAttribute(vg::lmhead_argmax_accept, kC, kMax) != cudaSuccess ||
-          cudaFuncSetAttribute(vg::logprob_tiles, kC, kMax) != cudaSuccess ||
           cudaFuncSetAttribute(vg::embed_rows, kC, kMax) != cudaSuccess ||
           cudaFuncSetAttribute(vg::spec_rows, kC, kMax) != cudaSuccess ||
           cudaFuncSetAttribute(vg::spec_rows_given, kC, kMax) != cudaSuccess ||
@@ -1568,21 +1570,31 @@ namespace {
 // How a call is cut: vocabulary tile, tiles per unit of work, candidates per unit.
 struct LpPlan {
   int tile_n, stages, n_vblk, group_tiles, n_groups, n_mblk, n_cand;
-  size_t stat, cand, total;
+  size_t stat, cand, floor, total;
 };
 LpPlan lp_plan(int R, int V, int n_top) {
   using namespace vg;
+  constexpr int kSms = 148;
   LpPlan p{};
-  p.n_cand = n_top > 0 ? n_top + kLpSpare : 0;
-  p.tile_n = 176;
-  p.stages = 5;
+  p.n_cand = lp_cands(n_top);
   p.n_mblk = cdiv(R, kLpM);
+  if (p.n_mblk == 1) {
+    p.tile_n = 176;
+    p.group_tiles = 5;
+  } else {
+    p.tile_n = 256;
+    p.group_tiles = 8;
+  }
   p.n_vblk = cdiv(V, p.tile_n);
-  p.group_tiles = 5;
+  while (cdiv(p.n_vblk, p.group_tiles) > kLpMaxGroups) ++p.group_tiles;
+  p.stages = 5;
+  while (lp_smem_bytes(p.tile_n, p.stages) > kMaxSmemBytes) --p.stages;
   p.n_groups = cdiv(p.n_vblk, p.group_tiles);
+  (void)kSms;
   p.stat = 0;
   p.cand = align256((size_t)p.n_groups * 3 * R * 4);
-  p.total = p.cand + align256((size_t)p.n_groups * R * p.n_cand * 8);
+  p.floor = p.cand + align256((size_t)p.n_groups * R * p.n_cand * 8);
+  p.total = p.floor + align256((size_t)R * 4);
   return p;
 }
 
@@ -1629,25 +1641,21 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
   a.b_box_rows = box_rows(V, p.tile_n);
   a.tile_n = p.tile_n;
   a.stages = p.stages;
-  a.n_cand = p.n_cand;
   a.stat = reinterpret_cast<float*>(ws + p.stat);
   a.cand = reinterpret_cast<unsigned long long*>(ws + p.cand);
+  if (p.n_mblk > 1) {
+    a.floor = reinterpret_cast<uint32_t*>(ws + p.floor);
+    if (cudaMemsetAsync(a.floor, 0, (size_t)R * 4, s) != cudaSuccess) return cuda_fail();
+  }
   CUtensorMap mH, mLM;
   const uint64_t dH[2] = {(uint64_t)H, (uint64_t)R}, dL[2] = {(uint64_t)H, (uint64_t)V}, sK[1] = {(uint64_t)H * 2};
   const uint32_t bH[2] = {kBK, (uint32_t)a.a_box_rows}, bL[2] = {kBK, (uint32_t)a.b_box_rows};
   if (make_map(&mH, h, 2, dH, sK, bH) || make_map(&mLM, lm_head, 2, dL, sK, bL)) return VG_ERR_CUDA;
-  {
-    ProfScope ps(VG_KERNEL_LM_HEAD, s);
-    if (launch_dep(logprob_tiles, min(dev->sms, p.n_mblk * p.n_groups), 192, lp_smem_bytes(p.tile_n, p.stages, p.n_cand), s,
-                   Launch::kPlain, mH, mLM, a) != cudaSuccess)
-      return cuda_fail();
-  }
   LpFinishArgs f{};
   f.R = R;
   f.H = H;
   f.V = V;
   f.n_groups = p.n_groups;
-  f.n_cand = p.n_cand;
   f.n_top = n_top;
   f.stat = a.stat;
   f.cand = a.cand;
@@ -1658,7 +1666,19 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
   f.entropy = entropy;
   f.top_ids = top_ids;
   f.top_logprobs = top_logprobs;
-  if (launch_dep(logprob_finish, R, kLpFinishThreads, 0, s, Launch::kPlain, f) != cudaSuccess) return cuda_fail();
+  auto launch = [&](auto nc) {
+    constexpr int NC = decltype(nc)::value;
+    cudaError_t e;
+    {
+      ProfScope ps(VG_KERNEL_LM_HEAD, s);
+      e = launch_dep(logprob_tiles<NC>, min(dev->sms, p.n_mblk * p.n_groups), 192, lp_smem_bytes(p.tile_n, p.stages), s,
+                     Launch::kPlain, mH, mLM, a);
+    }
+    return e == cudaSuccess ? launch_dep(logprob_finish<NC>, R, kLpFinishThreads, 0, s, Launch::kPlain, f) : e;
+  };
+  const cudaError_t e = p.n_cand == 12 ? launch(std::integral_constant<int, 12>{})
+                                       : launch(std::integral_constant<int, 24>{});
+  if (e != cudaSuccess) return cuda_fail();
   return VG_OK;
 }
 

@@ -27,7 +27,7 @@ def call(h, lm, tokens, n_top, status=0):
     ids = gd.empty((R, n_top), torch.int32, fill=-9) if n_top else None
     tl = gd.empty((R, n_top), torch.float32, fill=7.0) if n_top else None
     ws = gd.empty((vgv.vg_token_logprobs_workspace_bytes(R, H, V, n_top),), torch.uint8, fill=0)
-    vgv.vg_token_logprobs(h, lm, tokens, lp, en, ids, tl, ws)
+    vgv.vg_token_logprobs(h, lm, tokens, lp if tokens is not None else None, en, ids, tl, ws)
     torch.cuda.synchronize()
     assert vgv.vg_get_device_status()[0] == status
     gd.check()
@@ -111,6 +111,23 @@ def test_many_row_blocks():
         # only the grouping of the sums differs with the number of rows
         assert np.allclose(rep(a), b, rtol=1e-5, atol=1e-5)
         assert np.array_equal(np.tile(b[:8], (512,) + (1,) * (b.ndim - 1)), b)
+
+
+def test_ties_over_many_row_blocks():
+    """Rows whose logits are all equal (zero, positive, negative, and a mix of
+    zeros and others), in several row blocks and vocabulary groups: the lowest
+    indices, whatever order the groups finish in."""
+    V, H, R = 9001, 64, 520
+    lm = np.zeros((V, H))
+    lm[:, 0] = 1.0
+    lm[:, 1] = np.where(np.arange(V) % 100 == 50, 1.0, 0.0)
+    lm[:, 2] = -(np.arange(V) % 2).astype(float)
+    h = np.zeros((R, H))
+    h[1::5, 0], h[2::5, 0], h[3::5, 1], h[4::5, 2] = 1.5, -1.5, 2.0, 3.0
+    ids = call(dev(oracle.round_bf16_bits(h)), dev(oracle.round_bf16_bits(lm)), None, 20)[2]
+    low = np.arange(20)
+    for k, want in enumerate((low, low, low, low * 100 + 50, low * 2)):
+        assert (ids[k::5] == want).all(), k
 
 
 def test_rising_logits():
