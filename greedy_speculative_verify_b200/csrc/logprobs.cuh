@@ -48,12 +48,6 @@ __host__ __device__ constexpr int lp_smem_bytes(int tile_n, int stages) {
 // kernels are built for.
 __host__ __device__ constexpr int lp_cands(int n_top) { return n_top <= 8 ? 12 : 24; }
 
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // A row's best logits so far, descending (equal ones by index), in registers.
 template <int NC>
 struct LpList {
@@ -293,7 +287,7 @@ __global__ void __launch_bounds__(192, 1)
           for (int j = 0; j < kLpChunk; ++j) top = fmaxf(top, z[j]);
           const float now = fmaxf(m, top), base = now > -INFINITY ? now : 0.0f;
           if (now > m && m > -INFINITY) {  // to the new maximum
-            const float d = fmaxf(m - now, -1000.0f), f = ex2_approx(d * 1.4426950408889634f);
+            const float d = fmaxf(m - now, -1000.0f), f = ex2(d * 1.4426950408889634f);
             T = f * (T + S * d);
             S *= f;
           }
@@ -301,7 +295,7 @@ __global__ void __launch_bounds__(192, 1)
           float s1 = 0.0f, t1 = 0.0f;
 #pragma unroll
           for (int j = 0; j < kLpChunk; ++j) {
-            const float d = z[j] - base, e = ex2_approx(d * 1.4426950408889634f);
+            const float d = z[j] - base, e = ex2(d * 1.4426950408889634f);
             s1 += e;
             t1 = fmaf(e, fmaxf(d, -1000.0f), t1);  // a weight of 0 adds 0, also where z is -inf
           }

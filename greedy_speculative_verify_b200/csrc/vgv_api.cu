@@ -33,6 +33,8 @@ namespace {
 constexpr int kH = 1280, kI = 896, kE = 64, kS = 2, kTopK = 6;
 constexpr int kMaxDevices = 64;
 constexpr int kMaxSmemBytes = 232448;  // shared memory a CTA can ask for (227 KB)
+constexpr int kStaticSmemBytes = 1024;  // room for a kernel's static shared memory beside the dynamic
+constexpr int kKaMaxGrid = 256;     // CTAs of the 8-bit attention kernel at most
 constexpr int kEntryMaxGrid = 256;  // CTAs of the layer-entry kernel at most
 
 // Bytes of expert weights the layer entry prefetches into L2: the gate|up rows
@@ -154,6 +156,11 @@ vg_status device_state(DevState** out) {
       if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
               cudaSuccess)
+        return cuda_fail();
+    for (auto* k : {vg::kv8_attn<0, 64, 1>, vg::kv8_attn<0, 64, 2>, vg::kv8_attn<0, 128, 1>, vg::kv8_attn<0, 128, 2>,
+                    vg::kv8_attn<1, 64, 1>, vg::kv8_attn<1, 64, 2>, vg::kv8_attn<1, 128, 1>, vg::kv8_attn<1, 128, 2>})
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes - kStaticSmemBytes) !=
+          cudaSuccess)
         return cuda_fail();
     // Kernels that follow each other with dependent launches share SMs only if
     // their shared-memory configurations agree: every kernel of the decode
@@ -1308,10 +1315,20 @@ cudaError_t kv8_dispatch(int32_t format, int32_t dim, F&& f) {
 // one column of tensor-core tiles for up to 8 rows, else two.
 int kv8_nt(int rows, int group) { return rows * group <= 8 ? 1 : 2; }
 
-size_t kv8_attn_ws(const vg_kv8* c, int rows, int n_heads) {
-  const int group = n_heads / c->n_kv, nt = kv8_nt(rows, group), tiles = vg::cdiv(rows * group, 8 * nt);
-  return align256((size_t)c->B * c->n_kv * tiles * vg::cdiv(c->L_max, vg::kKaChunk) * 8 * nt * (2 + c->dim) * 4);
+// Partials of units split between CTAs (two slots a CTA), then the counters of
+// those units.
+struct KaWs {
+  size_t part, arrived, total;
+};
+KaWs kv8_attn_layout(const vg_kv8* c, int rows, int n_heads) {
+  const int nt = kv8_nt(rows, n_heads / c->n_kv);
+  KaWs L{};
+  L.arrived = 0;
+  L.part = align256((size_t)kKaMaxGrid * 4);
+  L.total = L.part + align256((size_t)2 * kKaMaxGrid * 8 * nt * (c->dim + 2) * 4);
+  return L;
 }
+size_t kv8_attn_ws(const vg_kv8* c, int rows, int n_heads) { return kv8_attn_layout(c, rows, n_heads).total; }
 
 vg_status kv8_attn_check(const vg_kv8* c, int32_t rows, int32_t n_heads) {
   const vg_status st = kv8_check(c);
@@ -1346,51 +1363,41 @@ vg_status kv8_append_launch(const vg_kv8* c, int32_t rows, const void* k, int64_
   return e == cudaSuccess ? VG_OK : cuda_fail();
 }
 
-vg_status kv8_attn_launch(const vg_kv8* c, int32_t rows, int32_t n_heads, const void* q, int64_t q_stride,
+vg_status kv8_attn_launch(DevState* dev, const vg_kv8* c, int32_t rows, int32_t n_heads, const void* q, int64_t q_stride,
                           const int32_t* lens, const int32_t* first, const int32_t* n_new, float scale, void* o,
                           int64_t o_stride, void* workspace, cudaStream_t s) {
   using namespace vg;
   const int group = n_heads / c->n_kv, nt = kv8_nt(rows, group);
+  const KaWs L = kv8_attn_layout(c, rows, n_heads);
   Kv8AttnArgs a{};
   a.c = kv8_view(c);
   a.rows = rows;
   a.n_heads = n_heads;
   a.n_tiles = cdiv(rows * group, 8 * nt);
+  a.stages = min(kKaStages, (kMaxSmemBytes - kStaticSmemBytes - ka_fixed_bytes(c->dim, nt)) / ka_stage_bytes(c->dim));
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
   a.lens = lens;
   a.first = first;
   a.n_new = n_new;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634 / (c->format == VG_KV8_INT8 ? 127.0 : 448.0));
-  a.part = static_cast<float*>(workspace);
-  a.n_chunks = cdiv(c->L_max, kKaChunk);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.part);
+  a.arrived = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.arrived);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.o_stride = o_stride;
-  const int units = c->B * c->n_kv * a.n_tiles;
-  auto chunks = [&](auto kern) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(units, a.n_chunks);
-    cfg.blockDim = dim3(32 * kKaWarps);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
-  };
-  const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
-    constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
-    cudaError_t r;
-    {
-      ProfScope ps(VG_KERNEL_ATTENTION, s);
-      r = nt == 1 ? chunks(kv8_attn_chunk<F, D, 1>) : chunks(kv8_attn_chunk<F, D, 2>);
-    }
-    if (r != cudaSuccess) return r;
-    return nt == 1 ? launch_dep(kv8_attn_merge<D, 1>, units * 8, D, 0, s, Launch::kPlain, a)
-                   : launch_dep(kv8_attn_merge<D, 2>, units * 16, D, 0, s, Launch::kPlain, a);
-  });
-  return e == cudaSuccess ? VG_OK : cuda_fail();
+  const int smem = ka_fixed_bytes(c->dim, nt) + a.stages * ka_stage_bytes(c->dim);
+  for (a.b0 = 0; a.b0 < c->B; a.b0 += kKaTable) {
+    a.nb = min(kKaTable, c->B - a.b0);
+    const int grid = min(dev->sms, kKaMaxGrid);
+    ProfScope ps(VG_KERNEL_ATTENTION, s);
+    const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
+      constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
+      return nt == 1 ? launch_dep(kv8_attn<F, D, 1>, grid, kKaThreads, smem, s, Launch::kPlain, a)
+                     : launch_dep(kv8_attn<F, D, 2>, grid, kKaThreads, smem, s, Launch::kPlain, a);
+    });
+    if (e != cudaSuccess) return cuda_fail();
+  }
+  return VG_OK;
 }
 
 }  // namespace
@@ -1477,7 +1484,7 @@ extern "C" vg_status vg_kv8_attn(const vg_kv8* c, int32_t rows, int32_t n_heads,
     return VG_ERR_WORKSPACE;
   DevState* dev = nullptr;
   if ((st = device_state(&dev)) != VG_OK) return st;
-  return kv8_attn_launch(c, rows, n_heads, q, q_stride, lens, first, n_new, scale, o, o_stride, workspace,
+  return kv8_attn_launch(dev, c, rows, n_heads, q, q_stride, lens, first, n_new, scale, o, o_stride, workspace,
                          reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -1554,7 +1561,7 @@ extern "C" vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* 
   if (launch_dep(attn_rope_append<true>, cdiv(R * kH / 2, 256), 256, 0, s, Launch::kPlain, a) != cudaSuccess)
     return cuda_fail();
   if ((st = kv8_append_launch(c, K + 1, qkv + kH, 3 * kH, qkv + 2 * kH, 3 * kH, lens, nullptr, s)) != VG_OK) return st;
-  if ((st = kv8_attn_launch(c, K + 1, kAttnHeads, qkv, 3 * kH, lens, nullptr, nullptr, 1.0f / sqrtf((float)kAttnDim), o,
+  if ((st = kv8_attn_launch(dev, c, K + 1, kAttnHeads, qkv, 3 * kH, lens, nullptr, nullptr, 1.0f / sqrtf((float)kAttnDim), o,
                             kH, ws + L.attn, s)) != VG_OK)
     return st;
   if (attn_project(o, w_o, R, kH, pk, s) != cudaSuccess) return cuda_fail();

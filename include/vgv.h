@@ -487,12 +487,17 @@ vg_status vg_kv8_read(const vg_kv8* c, int32_t rows, const int32_t* pos, const i
  * h / (n_heads / n_kv), at most 16 to a head. Rows i >= n_new[b] (n_new NULL:
  * none) are not read and get o = 0. lens[b] < 0, first[b] < 0, n_new[b] outside
  * [0, rows] or lens[b] + n_new[b] > L_max records VG_ERR_DEVICE_BOUNDS and gives
- * o = 0 for that sequence. scale > 0.
+ * o = 0 for that sequence. scale > 0; a row with scores beyond the fp32 range
+ * gets NaN.
  * Precision: codes enter both products exactly (f16 operands, fp32 sums), query
- * rows exactly down to 2^-29 of their largest element, softmax weights rounded
- * to 2^-12 of themselves; sums and maxima are fp32, o is rounded once.
- * workspace: vg_kv8_attn_workspace_bytes(c, rows, n_heads) bytes, 16-byte
- * aligned. Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED (rows > 8, more than
+ * rows exactly down to 2^-29 of their largest element; softmax weights are
+ * rounded to 2^-11 of themselves (those that, times their block's share of the
+ * largest value magnitude, are below 2^-23: to 2^-34); sums and maxima are
+ * fp32, o is rounded once.
+ * One launch for every 512 sequences. workspace: vg_kv8_attn_workspace_bytes(c,
+ * rows, n_heads) bytes, 16-byte aligned, ZERO-FILLED before its first call;
+ * every call leaves its counters zero again, so later calls (one at a time) need
+ * no clearing, unless one recorded VG_ERR_TIMEOUT. Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED (rows > 8, more than
  * 16 query heads to a key/value head), VG_ERR_WORKSPACE, VG_ERR_CUDA. */
 size_t vg_kv8_attn_workspace_bytes(const vg_kv8* c, int32_t rows, int32_t n_heads);
 vg_status vg_kv8_attn(const vg_kv8* c, int32_t rows, int32_t n_heads, const void* q, int64_t q_stride,
@@ -502,8 +507,8 @@ vg_status vg_kv8_attn(const vg_kv8* c, int32_t rows, int32_t n_heads, const void
 /* vg_attn_verify on an 8-bit cache (n_kv = 10, dim = 128, L_max <= 32768; B is
  * the cache's): the same layer, with the new rows' k (rotated) and v quantised
  * into the cache (vg_kv8_append at positions lens[b] ..) and the rows' attention
- * read from it (vg_kv8_attn, scale 1/sqrt(128)). Arguments and errors otherwise
- * as there; unlike there, an overflowing sequence's two device errors share the
+ * read from it (vg_kv8_attn, scale 1/sqrt(128); the workspace is zero-filled
+ * before its first call, as there). Arguments and errors otherwise as there; unlike there, an overflowing sequence's two device errors share the
  * status word. */
 size_t vg_attn_verify_kv8_workspace_bytes(const vg_kv8* c, int32_t K);
 vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* x, const void* w_qkv, const void* w_o,
