@@ -101,6 +101,13 @@ __device__ __forceinline__ void kv8_to_half(uint32_t x, uint32_t* lo, uint32_t* 
   }
 }
 
+// Four int8 codes + 128 as two pairs of f16 subnormals, (code + 128) * 2^-24.
+__device__ __forceinline__ void kv8_to_tiny(uint32_t x, uint32_t* lo, uint32_t* hi) {
+  x ^= 0x80808080u;
+  *lo = __byte_perm(x, 0u, 0x4140);
+  *hi = __byte_perm(x, 0u, 0x4342);
+}
+
 template <int FMT>
 __device__ __forceinline__ float4 kv8_to_float4(uint32_t x) {
   uint32_t lo, hi;

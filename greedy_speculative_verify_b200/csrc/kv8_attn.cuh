@@ -17,36 +17,33 @@
 // magnitude seen, so that none down to 2^-(14 + kKaLift) loses precision; the sum
 // of weights is taken in fp32 unrounded.
 //
-// Work: a unit is (sequence, kv head, 8 NT query rows), cut into tiles of 128
-// positions. All tiles of the batch form one list, of which every CTA (one per
-// SM) takes an equal contiguous share, whatever the lengths are. One warp feeds
-// a ring of tiles (two bulk copies each: a tile's keys, and its values, are
-// contiguous; the blocks' magnitudes beside them); warp w of the other eight
-// runs its own softmax over positions 16 w .. 16 w + 15 of every tile. At a
-// unit's end the warps are merged in shared memory. A unit that lies in several
-// CTAs' shares leaves partials, which the last of them to finish merges in CTA
-// order, so results do not depend on timing.
+// Work: a unit is (sequence, kv head, 8 NT query rows), cut into tiles of 16
+// positions a warp. All tiles of the batch form one list, of which every CTA
+// takes an equal contiguous share, whatever the lengths are. Warp w runs its own
+// softmax over positions 16 w .. 16 w + 15 of every tile, straight out of
+// registers: 16-byte loads, the next tile's keys requested as soon as this
+// tile's are used up, and its values likewise. At a unit's end the warps are
+// merged in shared memory. A unit that lies in several CTAs' shares leaves
+// partials, which the last of them to finish merges in CTA order, so results do
+// not depend on timing.
 #pragma once
 #include "attention.cuh"
 #include "kv8.cuh"
 
 namespace vg {
 
-constexpr int kKaWarps = 8;        // consumer warps
-constexpr int kKaTile = 16 * kKaWarps;  // positions per tile
-constexpr int kKaThreads = 32 * (kKaWarps + 1);
 constexpr int kKaMaxRows = 8;      // new rows per sequence
 constexpr int kKaMaxGroup = 16;    // query heads per kv head
 constexpr int kKaTable = 512;      // sequences per launch
-constexpr int kKaStages = 8;       // ring slots at most
 constexpr float kKaSlack = 6.0f;   // log2 of the largest weight
 constexpr float kKaLift = 512.0f;  // 2^9, on the f16 weights
+constexpr float kKaTiny = 5.9604645e-8f;  // 2^-24, the unit of f16 subnormals
 
 struct Kv8AttnArgs {
   Kv8View c;
   int32_t b0, nb;                // the launch's sequences: b0 .. b0 + nb - 1
   int32_t rows, n_heads, n_tiles;  // rows per sequence; n_tiles: 8 NT-row tiles of a kv head's rows * group query rows
-  int32_t stages;
+  int32_t block_log2;
   const __nv_bfloat16* q;
   int64_t q_stride;
   const int32_t* lens;   // [B] positions before the new rows
@@ -59,11 +56,10 @@ struct Kv8AttnArgs {
   int64_t o_stride;
 };
 
-__host__ __device__ constexpr int ka_stage_bytes(int dim) { return 2 * kKaTile * dim; }
-__host__ __device__ constexpr int ka_merge_bytes(int dim, int nt) { return kKaWarps * 8 * nt * (dim + 4 + 2) * 4; }
-__host__ __device__ constexpr int ka_fixed_bytes(int dim, int nt) {
-  return 1024 + kKaTable * 24 + 16 + ka_merge_bytes(dim, nt) + kKaStages * 16 * 4;
-}
+// Warps per CTA and CTAs per SM: 16 warps of at most 128 registers where a unit
+// has up to 8 query rows, 12 of at most 168 where it has 16.
+__host__ __device__ constexpr int ka_warps(int nt) { return nt == 1 ? 8 : 4; }
+__host__ __device__ constexpr int ka_ctas(int nt) { return nt == 1 ? 2 : 3; }
 
 // m16n8k16, f16 operands, fp32 accumulators; fragments as in mma_16816.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -103,6 +99,7 @@ struct Kv8Warp {
   uint32_t q[NT][DIM / 16][2];   // Q^T fragments
   float mult[NT][2];             // softmax scale * log2(e) / Q * 2^e of rows 2t, 2t+1
   int last[NT][2];               // last position those rows see (-1: none)
+  float bias[NT][2];             // int8: what the 128 in every code adds to a score's sum
   float m[NT][2], l[NT][2];      // running maximum (log2 units) and this lane's share of the sum
   float o[NT][DIM / 32][2][4];   // O^T: dimensions 4 (g + 8 j) + 0..3
   float top_v;                   // largest magnitude of a value block seen: o is in units of it / Q / kKaLift
@@ -137,17 +134,25 @@ struct Kv8Warp {
       // 2^(14 - floor(log2 big)), and its inverse (two factors: either may leave the normal range)
       const int ex = big > 0.0f && big < INFINITY ? ilogbf(big) : 0;
       const float up0 = exp2f((float)((14 - ex) / 2)), up1 = exp2f((float)((14 - ex) - (14 - ex) / 2));
+      float sum = 0.0f;
 #pragma unroll
       for (int k = 0; k < DIM / 16; ++k)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          q[nt][k][e] = pack_half2(bf16_lo(x[k][e]) * up0 * up1, bf16_hi(x[k][e]) * up0 * up1);
-      const float back = a.scale_log2 / up0 / up1;
+        for (int e = 0; e < 2; ++e) {
+          const __half2 h2 = __floats2half2_rn(bf16_lo(x[k][e]) * up0 * up1, bf16_hi(x[k][e]) * up0 * up1);
+          q[nt][k][e] = *reinterpret_cast<const uint32_t*>(&h2);
+          sum += __low2float(h2) + __high2float(h2);
+        }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sum *= kKaTiny * 128.0f;
+      const float back = a.scale_log2 / up0 / up1 * (FMT == kKv8Int8 ? 1.0f / kKaTiny : 1.0f);
       const int seen = real ? s.L + i : -1;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         mult[nt][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
         last[nt][e] = __shfl_sync(0xffffffffu, seen, 4 * (2 * t + e));
+        bias[nt][e] = FMT == kKv8Int8 ? __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e)) : 0.0f;
         m[nt][e] = -INFINITY;
         l[nt][e] = 0.0f;
       }
@@ -159,61 +164,69 @@ struct Kv8Warp {
     top_v = 0.0f;
   }
 
-  // 16 positions p0 .. p0 + 15, of which [lo, hi) are the sequence's: their keys
-  // and values (the group's bytes), and the magnitudes of their blocks. plain:
-  // every row sees all 16.
-  __device__ __forceinline__ void group16(const uint8_t* kb, const uint8_t* vb, float ks, float vs, int p0, int lo,
-                                          int hi, bool plain, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    const int tok = 4 * (g >> 1) + (g & 1);  // tile row g; row g + 8 is position tok + 2
-    float s[NT][4], s2[NT][4];
+  // A group of 16 positions in three steps: scores of its keys, weights, values.
+  // Keys in int8 enter as (code + 128) 2^-24, f16 subnormals that cost no
+  // subtraction; 128 times the row's sum is taken off the score. (Values do not:
+  // their weights are all positive, so the 128s would not cancel and the sums
+  // would lose what they add.)
+  __device__ __forceinline__ void scores(const uint4 (&kf)[DIM / 32], float (&s)[NT][4]) const {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.0f;
-    uint4 vf[DIM / 32];
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
 #pragma unroll
     for (int h = 0; h < DIM / 64; ++h) {
-      const uint4 ka = *reinterpret_cast<const uint4*>(kb + h * 1024 + tok * 64 + t * 16);
-      const uint4 kc = *reinterpret_cast<const uint4*>(kb + h * 1024 + (tok + 2) * 64 + t * 16);
+      const uint4 ka = kf[2 * h], kc = kf[2 * h + 1];
       const uint32_t xa[4] = {ka.x, ka.y, ka.z, ka.w}, xc[4] = {kc.x, kc.y, kc.z, kc.w};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t a0, a1, a2, a3;
-        kv8_to_half<FMT>(xa[w], &a0, &a2);
-        kv8_to_half<FMT>(xc[w], &a1, &a3);
+        if constexpr (FMT == kKv8Int8) {
+          kv8_to_tiny(xa[w], &a0, &a2);
+          kv8_to_tiny(xc[w], &a1, &a3);
+        } else {
+          kv8_to_half<FMT>(xa[w], &a0, &a2);
+          kv8_to_half<FMT>(xc[w], &a1, &a3);
+        }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)  // two chains of sums
-          mma_f16(w & 1 ? s2[nt] : s[nt], a0, a1, a2, a3, q[nt][h * 4 + w][0], q[nt][h * 4 + w][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, q[nt][h * 4 + w][0], q[nt][h * 4 + w][1]);
       }
     }
-#pragma unroll
-    for (int j = 0; j < DIM / 32; ++j) vf[j] = *reinterpret_cast<const uint4*>(vb + (g + 8 * j) * 64 + t * 16);
-    // ---- weights
-    float z[NT][2][2];
+  }
+
+  // ks, vs: the magnitudes of the positions' blocks. plain: every row sees all of
+  // p0 .. p0 + 15.
+  __device__ __forceinline__ void weights(float (&s)[NT][4], float ks, float vs, int p0, int lo, bool plain, int lane,
+                                          uint32_t (&b0)[NT], uint32_t (&b1)[NT]) {
+    const int tok = 4 * (lane >> 3) + ((lane >> 2) & 1);  // tile row g = lane / 4; row g + 8 is position tok + 2
     bool above = vs > top_v;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float mu[2] = {mult[nt][0] * ks, mult[nt][1] * ks};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = (FMT == kKv8Int8 ? s[nt][e] - bias[nt][e & 1] : s[nt][e]) * mu[e & 1];
+    }
+    if (!plain) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int p = p0 + tok + (e & 2);
+          if (p < lo || p > last[nt][e & 1]) s[nt][e] = -INFINITY;
+        }
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float mu = mult[nt][e] * ks;
-        z[nt][e][0] = (s[nt][e] + s2[nt][e]) * mu;
-        z[nt][e][1] = (s[nt][2 + e] + s2[nt][2 + e]) * mu;
-        if (!plain) {
-          const int pa = p0 + tok, pc = pa + 2;
-          if (pa < lo || pa > last[nt][e]) z[nt][e][0] = -INFINITY;
-          if (pc < lo || pc > last[nt][e]) z[nt][e][1] = -INFINITY;
-        }
-        above |= fmaxf(z[nt][e][0], z[nt][e][1]) > m[nt][e] + kKaSlack;
-      }
-    if (__any_sync(0xffffffffu, above)) {  // new maxima (or a larger value scale)
+      for (int e = 0; e < 2; ++e) above |= fmaxf(s[nt][e], s[nt][2 + e]) > m[nt][e] + kKaSlack;
+    if (__any_sync(0xffffffffu, above)) {  // new maxima (or a larger value magnitude)
       const float grow_v = vs > top_v ? top_v / vs : 1.0f;
       top_v = fmaxf(top_v, vs);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(z[nt][e][0], z[nt][e][1]);
+          float mx = fmaxf(s[nt][e], s[nt][2 + e]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -230,32 +243,38 @@ struct Kv8Warp {
           }
         }
     }
-    const float share = top_v > 0.0f ? vs / top_v * kKaLift : 0.0f;
-    uint32_t b0[NT], b1[NT];
+    float share = kKaLift;
+    if (vs != top_v) share = top_v > 0.0f ? vs / top_v * kKaLift : 0.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float w[2][2];
+      float w[4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float base = m[nt][e] > -INFINITY ? m[nt][e] : 0.0f;
-        w[e][0] = ex2(z[nt][e][0] - base);
-        w[e][1] = ex2(z[nt][e][1] - base);
-        l[nt][e] += w[e][0] + w[e][1];
+      for (int e = 0; e < 4; ++e) {
+        const float base = m[nt][e & 1] > -INFINITY ? m[nt][e & 1] : 0.0f;
+        w[e] = ex2(s[nt][e] - base);
       }
+      l[nt][0] += w[0] + w[2];
+      l[nt][1] += w[1] + w[3];
       // rows 2t, 2t+1 of positions g, g + 8 -> positions 2t, 2t+1 (+ 8) of row g
-      b0[nt] = movmatrix_trans(pack_half2(w[0][0] * share, w[1][0] * share));
-      b1[nt] = movmatrix_trans(pack_half2(w[0][1] * share, w[1][1] * share));
+      b0[nt] = movmatrix_trans(pack_half2(w[0] * share, w[1] * share));
+      b1[nt] = movmatrix_trans(pack_half2(w[2] * share, w[3] * share));
     }
-    // ---- values
-    if (FMT == kKv8E4m3 && p0 + kKv8Group > hi) {  // a code never written may be NaN, and 0 * NaN is not 0
-      const int real = hi - p0 - 4 * t;            // of this lane's four positions
-      const uint32_t keep = real >= 4 ? 0xFFFFFFFFu : real <= 0 ? 0u : (1u << (8 * real)) - 1u;
-#pragma unroll
-      for (int j = 0; j < DIM / 32; ++j) vf[j].x &= keep, vf[j].y &= keep, vf[j].z &= keep, vf[j].w &= keep;
+  }
+
+  // real: how many of the group's positions are the sequence's
+  __device__ __forceinline__ void values(const uint4 (&vf)[DIM / 32], const uint32_t (&b0)[NT], const uint32_t (&b1)[NT],
+                                         int real, int lane) {
+    uint32_t keep = 0xFFFFFFFFu;
+    if (FMT == kKv8E4m3 && real < kKv8Group) {  // a code never written may be NaN, and 0 * NaN is not 0
+      const int mine = real - 4 * (lane & 3);
+      keep = mine >= 4 ? 0xFFFFFFFFu : mine <= 0 ? 0u : (1u << (8 * mine)) - 1u;
     }
 #pragma unroll
     for (int j = 0; j < DIM / 32; ++j) {
-      const uint32_t x[4] = {vf[j].x, vf[j].y, vf[j].z, vf[j].w};
+      uint32_t x[4] = {vf[j].x, vf[j].y, vf[j].z, vf[j].w};
+      if (FMT == kKv8E4m3)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] &= keep;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         uint32_t a0, a1, a2, a3;
@@ -274,47 +293,31 @@ struct KaPlace {
   int j, n;          // tile of the unit, and how many it has
 };
 
-__device__ __forceinline__ void ka_bar() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kKaWarps) : "memory"); }
-
-// Four bytes global -> shared, asynchronous; ka_cp_arrive makes the barrier see
-// this lane's copies complete (one arrival, counted at initialisation).
-__device__ __forceinline__ void ka_cp4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void ka_cp_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+// 16 bytes read once: not kept in L1.
+__device__ __forceinline__ uint4 ka_ld(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
 }
 
 template <int FMT, int DIM, int NT>
-__global__ void __launch_bounds__(kKaThreads, 1) kv8_attn(const Kv8AttnArgs a) {
-  constexpr int kTileBytes = kKaTile * DIM, kRowW = DIM + 4;
-  extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* ring = smem;  // [stages][keys | values]
-  uint8_t* at = smem + a.stages * ka_stage_bytes(DIM);
-  float* wo = reinterpret_cast<float*>(at);                 // [kKaWarps][8 NT][kRowW]
-  float* wm = wo + kKaWarps * 8 * NT * kRowW;               // [kKaWarps][8 NT]
-  float* wl = wm + kKaWarps * 8 * NT;
-  float* mag = wl + kKaWarps * 8 * NT;                      // [stages][keys 8 | values 8]
-  int64_t* start = reinterpret_cast<int64_t*>(mag + kKaStages * 16);  // [kKaTable + 1] first tile of each sequence
-  int4* span = reinterpret_cast<int4*>(start + kKaTable + 2);         // [kKaTable] lo, hi, L, n
-  __shared__ __align__(8) uint64_t full[kKaStages], empty[kKaStages];
+__global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const Kv8AttnArgs a) {
+  constexpr int W = ka_warps(NT), kThreads = 32 * W, kTile = kKv8Group * W, kRowW = DIM + 4;
+  __shared__ __align__(16) float wo[W * 8 * NT * kRowW];
+  __shared__ float wm[W * 8 * NT], wl[W * 8 * NT];
+  __shared__ int64_t start[kKaTable + 1];  // first tile of each sequence
+  __shared__ int4 span[kKaTable];          // lo, hi, L, n
   __shared__ int64_t sums[kKaTable / 32];
   __shared__ int last_s;
-  __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.n_heads / a.c.n_kv, units = a.c.n_kv * a.n_tiles;  // units per sequence
   griddep_launch_dependents();
-  if (tid == 0) {
-    for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&full[i], 1 + 16);
-      mbar_init(&empty[i], kKaWarps);
-    }
-    abort_flag = 0;
-    fence_mbar_init();
-  }
   griddep_wait();
   // ---- the list of tiles: every sequence's range and first tile
-  for (int c = warp; c * 32 < a.nb; c += kKaWarps + 1) {
+  for (int c = warp; c * 32 < a.nb; c += W) {
     const int i = c * 32 + lane;
     int64_t n = 0;
     if (i < a.nb) {
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv8_attn(const Kv8AttnArgs a) {
       if (!kv8_span(a, a.b0 + i, &s) && blockIdx.x == 0) record_error(kErrBounds, 343);
       span[i] = make_int4(s.lo, s.hi, s.L, s.n);
       // an empty sequence has one tile a unit, without positions: its rows become 0
-      n = (int64_t)units * max(1, cdiv(s.hi - s.lo / kKv8Group * kKv8Group, kKaTile));
+      n = (int64_t)units * max(1, cdiv(s.hi - s.lo / kKv8Group * kKv8Group, kTile));
     }
     int64_t sum = n;
 #pragma unroll
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv8_attn(const Kv8AttnArgs a) {
     if (lane == 31) sums[c] = sum;
   }
   __syncthreads();
-  for (int i = tid; i <= a.nb; i += kKaThreads) {
+  for (int i = tid; i <= a.nb; i += kThreads) {
     int64_t before = 0;
     for (int c = 0; c < (i < a.nb ? i / 32 : cdiv(a.nb, 32)); ++c) before += sums[c];
     start[i] = (i < a.nb ? start[i] : 0) + before;
@@ -343,7 +346,6 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv8_attn(const Kv8AttnArgs a) {
   // G CTAs with a share each, none of it empty (the count of a split unit's CTAs relies on that)
   const int64_t total = start[a.nb], G = min((int64_t)gridDim.x, total);
   const int64_t t0 = blockIdx.x < G ? total * blockIdx.x / G : 0, t1 = blockIdx.x < G ? total * (blockIdx.x + 1) / G : 0;
-  const uint64_t limit = g_wait_timeout_ns;
   auto place = [&](int64_t T, int b) {  // tile T, in sequence b or a later one
     while (T >= start[b + 1]) ++b;
     KaPlace p;
@@ -365,103 +367,68 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv8_attn(const Kv8AttnArgs a) {
     }
     return place(T, lo);
   };
-  auto advance = [&](KaPlace& p) {  // to the next tile
-    if (++p.j < p.n) return;
-    p.j = 0;
-    if (++p.tile < a.n_tiles) return;
-    p.tile = 0;
-    if (++p.kvh < a.c.n_kv) return;
-    p.kvh = 0;
-    if (++p.b < a.nb) p.n = (int)((start[p.b + 1] - start[p.b]) / units);
-  };
-  const size_t blocks = a.c.L_max / a.c.block;
+  const size_t blocks = (size_t)a.c.L_max >> a.block_log2;
+  const int g = lane >> 2, t = lane & 3;
+  // this lane's bytes in a group: of the keys positions tok and tok + 2, of the values 4 dimensions of 4 positions
+  const int k_at = (4 * (g >> 1) + (g & 1)) * 64 + t * 16, v_at = lane * 16;
 
-  if (t0 < t1) {
-    if (warp == kKaWarps) {
-      // ---- producer
-      KaPlace p = locate(t0);
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, last_par = 0;
-      for (int64_t T = t0; T < t1; ++T) {
-        bool go = true;
-        if (lane == 0) go = !abort_flag && mbar_wait(&empty[stage], phase ^ 1, limit);
-        go = __shfl_sync(0xffffffffu, go, 0);
-        __syncwarp();
-        if (!go) {
-          if (lane == 0 && !abort_flag) record_error(kErrTimeout, 344);
-          abort_flag = 1;
-          break;
-        }
-        const int4 s = span[p.b];
-        const int p0 = s.x / kKv8Group * kKv8Group + p.j * kKaTile;
-        const int groups = max(0, min(kKaWarps, cdiv(s.y - p0, kKv8Group)));
-        const size_t head = (size_t)(a.b0 + p.b) * a.c.n_kv + p.kvh;
-        if (lane == 0) {
-          const uint32_t bytes = (uint32_t)groups * kKv8Group * DIM;
-          mbar_arrive_expect_tx(&full[stage], 2 * bytes);
-          if (bytes) {
-            uint8_t* dst = ring + stage * ka_stage_bytes(DIM);
-            const size_t src = (head * a.c.L_max + p0) * DIM;
-            bulk_load(dst, a.c.k + src, bytes, &full[stage]);
-            bulk_load(dst + kTileBytes, a.c.v + src, bytes, &full[stage]);
-          }
-        }
-        if (lane < 16) {  // the magnitude of each group's block
-          const int gi = lane & 7;
-          if (gi < groups)
-            ka_cp4(mag + stage * 16 + lane, (lane < 8 ? a.c.k_amax : a.c.v_amax) + head * blocks + (p0 + gi * kKv8Group) / a.c.block);
-          ka_cp_arrive(&full[stage]);
-        }
-        issued |= 1u << stage;
-        last_par = (last_par & ~(1u << stage)) | (phase << stage);
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1;
-        }
-        advance(p);
+  int b_at = 0;
+  for (int64_t T = t0; T < t1;) {
+    const KaPlace p = T == t0 ? locate(T) : place(T, b_at);
+    b_at = p.b;
+    const int4 sp = span[p.b];
+    const Kv8Span s{sp.z, sp.x, sp.y, sp.w};
+    const int64_t seg0 = T - p.j, seg1 = seg0 + p.n;  // the unit's tiles
+    const int n = (int)(min(seg1, t1) - T);           // those of this CTA
+    int p0 = s.lo / kKv8Group * kKv8Group + p.j * kTile + warp * kKv8Group;
+    const size_t head = (size_t)(a.b0 + p.b) * a.c.n_kv + p.kvh;
+    const uint8_t* kp = a.c.k + (head * a.c.L_max + p0) * DIM + k_at;
+    const uint8_t* vp = a.c.v + (head * a.c.L_max + p0) * DIM + v_at;
+    const float *ka = a.c.k_amax + head * blocks, *va = a.c.v_amax + head * blocks;
+    uint4 kf[DIM / 32], vf[DIM / 32];
+    float ks = 0.0f, vs = 0.0f;
+    auto load_k = [&]() {
+#pragma unroll
+      for (int h = 0; h < DIM / 64; ++h) {
+        kf[2 * h] = ka_ld(kp + h * 1024);
+        kf[2 * h + 1] = ka_ld(kp + h * 1024 + 128);
       }
-      // every copy has landed before the CTA exits (also after a timeout)
-      if (lane == 0)
-        for (int i = 0; i < a.stages; ++i)
-          if (issued & (1u << i)) mbar_wait(&full[i], (last_par >> i) & 1, limit);
-    } else {
-      // ---- consumers
-      KaPlace p = locate(t0);
-      int stage = 0;
-      uint32_t phase = 0;
-      Kv8Warp<FMT, DIM, NT> w;
-      bool fresh = true;
-      int64_t seg0 = t0 - p.j;  // the unit's first tile
-      for (int64_t T = t0; T < t1; ++T) {
-        const int4 sp = span[p.b];
-        const Kv8Span s{sp.z, sp.x, sp.y, sp.w};
-        if (fresh) {
-          w.init(a, a.b0 + p.b, p.kvh, p.tile, s, lane);
-          seg0 = T - p.j;
-          fresh = false;
-        }
-        const bool go = __all_sync(0xffffffffu, !abort_flag && mbar_wait(&full[stage], phase, limit));
-        if (!go) {  // the loop goes on without the data, so that the barriers below stay met
-          if (!abort_flag) record_error(kErrTimeout, 345);
-          abort_flag = 1;
-        } else {
-          const int p0 = s.lo / kKv8Group * kKv8Group + p.j * kKaTile + warp * kKv8Group;
-          if (p0 < s.hi) {
-            const uint8_t* kb = ring + stage * ka_stage_bytes(DIM) + warp * kKv8Group * DIM;
-            w.group16(kb, kb + kTileBytes, mag[stage * 16 + warp], mag[stage * 16 + 8 + warp], p0, s.lo, s.hi,
-                      p0 >= s.lo && p0 + kKv8Group - 1 <= s.L, lane);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[stage]);
-        }
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1;
-        }
-        const bool ends = p.j == p.n - 1;
-        if (ends || T == t1 - 1) {
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int j = 0; j < DIM / 32; ++j) vf[j] = ka_ld(vp + j * 512);
+    };
+    if (p0 < s.hi) {
+      load_k();
+      load_v();
+      ks = ka[p0 >> a.block_log2];
+      vs = va[p0 >> a.block_log2];
+    }
+    Kv8Warp<FMT, DIM, NT> w;
+    w.init(a, a.b0 + p.b, p.kvh, p.tile, s, lane);
+    for (int i = 0; i < n && p0 < s.hi; ++i) {
+      const bool more = i + 1 < n && p0 + kTile < s.hi;
+      float z[NT][4];
+      uint32_t b0[NT], b1[NT];
+      w.scores(kf, z);
+      const float ks_now = ks, vs_now = vs;
+      if (more) {
+        kp += kTile * DIM;
+        load_k();
+        ks = ka[(p0 + kTile) >> a.block_log2];
+        vs = va[(p0 + kTile) >> a.block_log2];
+      }
+      w.weights(z, ks_now, vs_now, p0, s.lo, p0 >= s.lo && p0 + kKv8Group - 1 <= s.L, lane, b0, b1);
+      w.values(vf, b0, b1, s.hi - p0, lane);
+      if (more) {
+        vp += kTile * DIM;
+        load_v();
+      }
+      p0 += kTile;
+    }
+    T += n;
+    const bool ends = T == seg1;
           // ---- merge the warps
-          const int g = lane >> 2, t = lane & 3;
           const float back = w.top_v / (kv8_q<FMT>() * kKaLift);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -482,8 +449,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv8_attn(const Kv8AttnArgs a) {
                     make_float4(w.o[nt][j][0][e] * back, w.o[nt][j][0][2 + e] * back, w.o[nt][j][1][e] * back,
                                 w.o[nt][j][1][2 + e] * back);
             }
-          ka_bar();
-          const int64_t seg1 = seg0 + p.n;
+          __syncthreads();
           const bool whole = seg0 >= t0 && ends;
           float* slot = a.part + (size_t)(2 * blockIdx.x + (seg0 < t0 ? 0 : 1)) * (8 * NT) * (DIM + 2);
           const int n_q = s.n * group;
@@ -496,15 +462,15 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv8_attn(const Kv8AttnArgs a) {
             *reinterpret_cast<uint2*>(a.o + ((int64_t)(a.b0 + p.b) * a.rows + i) * a.o_stride + h * DIM + d) =
                 make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
           };
-          for (int i = tid; i < 8 * NT * (DIM / 4); i += 32 * kKaWarps) {
+          for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
             const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
             float mm = -INFINITY, ls = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kKaWarps; ++k) mm = fmaxf(mm, wm[k * 8 * NT + r]);
+            for (int k = 0; k < W; ++k) mm = fmaxf(mm, wm[k * 8 * NT + r]);
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (mm > -INFINITY) {
 #pragma unroll
-              for (int k = 0; k < kKaWarps; ++k) {
+              for (int k = 0; k < W; ++k) {
                 const float f = ex2(wm[k * 8 * NT + r] - mm);
                 const float4 v = *reinterpret_cast<const float4*>(wo + (k * 8 * NT + r) * kRowW + d);
                 ls += wl[k * 8 * NT + r] * f;
@@ -524,12 +490,12 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv8_attn(const Kv8AttnArgs a) {
             // the unit's CTAs: those whose shares hold its first and its last tile
             const int64_t c0 = ((seg0 + 1) * G - 1) / total, c1 = (seg1 * G - 1) / total;
             __threadfence();
-            ka_bar();
+            __syncthreads();
             if (tid == 0) last_s = atomicAdd(a.arrived + c0, 1u) == (uint32_t)(c1 - c0);
-            ka_bar();
+            __syncthreads();
             if (last_s) {
               __threadfence();
-              for (int i = tid; i < 8 * NT * (DIM / 4); i += 32 * kKaWarps) {
+              for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
                 const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
                 float mm = -INFINITY, ls = 0.0f;
                 float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -550,14 +516,8 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv8_attn(const Kv8AttnArgs a) {
               if (tid == 0) atomicExch(a.arrived + c0, 0u);
             }
           }
-          ka_bar();  // the merge buffers are free again
-          fresh = true;
-        }
-        advance(p);
-      }
-    }
+          __syncthreads();  // the merge buffers are free again
   }
-  __syncthreads();
 }
 
 }  // namespace vg

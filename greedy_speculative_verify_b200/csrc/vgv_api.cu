@@ -33,8 +33,7 @@ namespace {
 constexpr int kH = 1280, kI = 896, kE = 64, kS = 2, kTopK = 6;
 constexpr int kMaxDevices = 64;
 constexpr int kMaxSmemBytes = 232448;  // shared memory a CTA can ask for (227 KB)
-constexpr int kStaticSmemBytes = 1024;  // room for a kernel's static shared memory beside the dynamic
-constexpr int kKaMaxGrid = 256;     // CTAs of the 8-bit attention kernel at most
+constexpr int kKaMaxGrid = 512;     // CTAs of the 8-bit attention kernel at most
 constexpr int kEntryMaxGrid = 256;  // CTAs of the layer-entry kernel at most
 
 // Bytes of expert weights the layer entry prefetches into L2: the gate|up rows
@@ -156,11 +155,6 @@ vg_status device_state(DevState** out) {
       if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
               cudaSuccess)
-        return cuda_fail();
-    for (auto* k : {vg::kv8_attn<0, 64, 1>, vg::kv8_attn<0, 64, 2>, vg::kv8_attn<0, 128, 1>, vg::kv8_attn<0, 128, 2>,
-                    vg::kv8_attn<1, 64, 1>, vg::kv8_attn<1, 64, 2>, vg::kv8_attn<1, 128, 1>, vg::kv8_attn<1, 128, 2>})
-      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes - kStaticSmemBytes) !=
-          cudaSuccess)
         return cuda_fail();
     // Kernels that follow each other with dependent launches share SMs only if
     // their shared-memory configurations agree: every kernel of the decode
@@ -1374,7 +1368,7 @@ vg_status kv8_attn_launch(DevState* dev, const vg_kv8* c, int32_t rows, int32_t 
   a.rows = rows;
   a.n_heads = n_heads;
   a.n_tiles = cdiv(rows * group, 8 * nt);
-  a.stages = min(kKaStages, (kMaxSmemBytes - kStaticSmemBytes - ka_fixed_bytes(c->dim, nt)) / ka_stage_bytes(c->dim));
+  for (a.block_log2 = 4; (1 << a.block_log2) < c->block;) ++a.block_log2;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
   a.lens = lens;
@@ -1385,15 +1379,14 @@ vg_status kv8_attn_launch(DevState* dev, const vg_kv8* c, int32_t rows, int32_t 
   a.arrived = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.arrived);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.o_stride = o_stride;
-  const int smem = ka_fixed_bytes(c->dim, nt) + a.stages * ka_stage_bytes(c->dim);
   for (a.b0 = 0; a.b0 < c->B; a.b0 += kKaTable) {
     a.nb = min(kKaTable, c->B - a.b0);
-    const int grid = min(dev->sms, kKaMaxGrid);
+    const int grid = min(dev->sms * ka_ctas(nt), kKaMaxGrid), threads = 32 * ka_warps(nt);
     ProfScope ps(VG_KERNEL_ATTENTION, s);
     const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
       constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
-      return nt == 1 ? launch_dep(kv8_attn<F, D, 1>, grid, kKaThreads, smem, s, Launch::kPlain, a)
-                     : launch_dep(kv8_attn<F, D, 2>, grid, kKaThreads, smem, s, Launch::kPlain, a);
+      return nt == 1 ? launch_dep(kv8_attn<F, D, 1>, grid, threads, 0, s, Launch::kPlain, a)
+                     : launch_dep(kv8_attn<F, D, 2>, grid, threads, 0, s, Launch::kPlain, a);
     });
     if (e != cudaSuccess) return cuda_fail();
   }
