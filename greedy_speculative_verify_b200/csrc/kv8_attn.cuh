@@ -104,8 +104,9 @@ struct Kv8Warp {
   float o[NT][DIM / 32][2][4];   // O^T: dimensions 4 (g + 8 j) + 0..3
   float top_v;                   // largest magnitude of a value block seen: o is in units of it / Q / kKaLift
 
-  __device__ __forceinline__ void init(const Kv8AttnArgs& a, int b, int kvh, int tile, const Kv8Span& s, int lane) {
-    const int g = lane >> 2, t = lane & 3, group = a.n_heads / a.c.n_kv, n_q = s.n * group;
+  // The tile's query rows, 16 dimensions of every 64 a lane; zeros behind the real ones.
+  __device__ __forceinline__ void load(const Kv8AttnArgs& a, int b, int kvh, int tile, int n_q, int lane) {
+    const int g = lane >> 2, t = lane & 3, group = a.n_heads / a.c.n_kv;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       // column g of the tile: query row r = i * group + head in the group
@@ -113,33 +114,40 @@ struct Kv8Warp {
       const bool real = r < n_q;
       const int i = real ? r / group : 0, h = kvh * group + (real ? r - i * group : 0);
       const __nv_bfloat16* src = a.q + ((int64_t)b * a.rows + i) * a.q_stride + h * DIM + 16 * t;
-      uint32_t x[DIM / 16][4];
-      float big = 0.0f;
 #pragma unroll
-      for (int s16 = 0; s16 < DIM / 64; ++s16) {
+      for (int k = 0; k < DIM / 64; ++k) {
         uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
         if (real) {
-          w0 = *reinterpret_cast<const uint4*>(src + 64 * s16);
-          w1 = *reinterpret_cast<const uint4*>(src + 64 * s16 + 8);
+          w0 = *reinterpret_cast<const uint4*>(src + 64 * k);
+          w1 = *reinterpret_cast<const uint4*>(src + 64 * k + 8);
         }
-        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[s16 * 4 + e / 2][e % 2] = w[e];
-          big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-        }
+        q[nt][4 * k][0] = w0.x, q[nt][4 * k][1] = w0.y, q[nt][4 * k + 1][0] = w0.z, q[nt][4 * k + 1][1] = w0.w;
+        q[nt][4 * k + 2][0] = w1.x, q[nt][4 * k + 2][1] = w1.y, q[nt][4 * k + 3][0] = w1.z, q[nt][4 * k + 3][1] = w1.w;
       }
+    }
+  }
+
+  // Turns the loaded rows into f16 fragments and clears the sums.
+  __device__ __forceinline__ void begin(const Kv8AttnArgs& a, int tile, const Kv8Span& s, int lane) {
+    const int g = lane >> 2, t = lane & 3, group = a.n_heads / a.c.n_kv, n_q = s.n * group;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float big = 0.0f;
+#pragma unroll
+      for (int k = 0; k < DIM / 16; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) big = fmaxf(big, fmaxf(fabsf(bf16_lo(q[nt][k][e])), fabsf(bf16_hi(q[nt][k][e]))));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      // 2^(14 - floor(log2 big)), and its inverse (two factors: either may leave the normal range)
-      const int ex = big > 0.0f && big < INFINITY ? ilogbf(big) : 0;
-      const float up0 = exp2f((float)((14 - ex) / 2)), up1 = exp2f((float)((14 - ex) - (14 - ex) / 2));
+      // 2^(14 - floor(log2 big)), as two factors: the product may leave the normal range
+      const int ex = big > 0.0f && big < INFINITY ? ilogbf(big) : 0, lift = 14 - ex;
+      const float up0 = __int_as_float((lift / 2 + 127) << 23), up1 = __int_as_float((lift - lift / 2 + 127) << 23);
       float sum = 0.0f;
 #pragma unroll
       for (int k = 0; k < DIM / 16; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const __half2 h2 = __floats2half2_rn(bf16_lo(x[k][e]) * up0 * up1, bf16_hi(x[k][e]) * up0 * up1);
+          const __half2 h2 = __floats2half2_rn(bf16_lo(q[nt][k][e]) * up0 * up1, bf16_hi(q[nt][k][e]) * up0 * up1);
           q[nt][k][e] = *reinterpret_cast<const uint32_t*>(&h2);
           sum += __low2float(h2) + __high2float(h2);
         }
@@ -147,7 +155,7 @@ struct Kv8Warp {
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       sum *= kKaTiny * 128.0f;
       const float back = a.scale_log2 / up0 / up1 * (FMT == kKv8Int8 ? 1.0f / kKaTiny : 1.0f);
-      const int seen = real ? s.L + i : -1;
+      const int r = (tile * NT + nt) * 8 + g, seen = r < n_q ? s.L + r / group : -1;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         mult[nt][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
@@ -303,15 +311,29 @@ __device__ __forceinline__ uint4 ka_ld(const uint8_t* p) {
   return v;
 }
 
+// o of row r of p's tile, dimensions d .. d + 3, from the weighted values and the
+// sum of weights; rows from n_q on are not real: 0.
+template <int DIM, int NT>
+__device__ __forceinline__ void ka_store(const Kv8AttnArgs& a, const KaPlace& p, int n_q, int r, int d, float4 v, float l) {
+  const int group = a.n_heads / a.c.n_kv, rr = p.tile * 8 * NT + r;
+  if (rr >= a.rows * group) return;
+  const int i = rr / group, h = p.kvh * group + rr - i * group;
+  const float inv = rr < n_q && l != 0.0f ? 1.0f / l : 0.0f;  // NaN sums stay NaN
+  if (inv == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const __nv_bfloat162 x = __floats2bfloat162_rn(v.x * inv, v.y * inv), y = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+  *reinterpret_cast<uint2*>(a.o + ((int64_t)(a.b0 + p.b) * a.rows + i) * a.o_stride + h * DIM + d) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+
 template <int FMT, int DIM, int NT>
 __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const Kv8AttnArgs a) {
   constexpr int W = ka_warps(NT), kThreads = 32 * W, kTile = kKv8Group * W, kRowW = DIM + 4;
   __shared__ __align__(16) float wo[W * 8 * NT * kRowW];
   __shared__ float wm[W * 8 * NT], wl[W * 8 * NT];
-  __shared__ int64_t start[kKaTable + 1];  // first tile of each sequence
+  __shared__ int start[kKaTable + 1];  // first tile of each sequence
   __shared__ int4 span[kKaTable];          // lo, hi, L, n
-  __shared__ int64_t sums[kKaTable / 32];
-  __shared__ int last_s;
+  __shared__ int sums[kKaTable / 32];
+  __shared__ int last_s[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.n_heads / a.c.n_kv, units = a.c.n_kv * a.n_tiles;  // units per sequence
   griddep_launch_dependents();
@@ -319,18 +341,18 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
   // ---- the list of tiles: every sequence's range and first tile
   for (int c = warp; c * 32 < a.nb; c += W) {
     const int i = c * 32 + lane;
-    int64_t n = 0;
+    int n = 0;
     if (i < a.nb) {
       Kv8Span s;
       if (!kv8_span(a, a.b0 + i, &s) && blockIdx.x == 0) record_error(kErrBounds, 343);
       span[i] = make_int4(s.lo, s.hi, s.L, s.n);
       // an empty sequence has one tile a unit, without positions: its rows become 0
-      n = (int64_t)units * max(1, cdiv(s.hi - s.lo / kKv8Group * kKv8Group, kTile));
+      n = units * max(1, cdiv(s.hi - s.lo / kKv8Group * kKv8Group, kTile));
     }
-    int64_t sum = n;
+    int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
     if (i < a.nb) start[i] = sum - n;
@@ -338,27 +360,34 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
   }
   __syncthreads();
   for (int i = tid; i <= a.nb; i += kThreads) {
-    int64_t before = 0;
+    int before = 0;
     for (int c = 0; c < (i < a.nb ? i / 32 : cdiv(a.nb, 32)); ++c) before += sums[c];
     start[i] = (i < a.nb ? start[i] : 0) + before;
   }
   __syncthreads();
-  // G CTAs with a share each, none of it empty (the count of a split unit's CTAs relies on that)
-  const int64_t total = start[a.nb], G = min((int64_t)gridDim.x, total);
-  const int64_t t0 = blockIdx.x < G ? total * blockIdx.x / G : 0, t1 = blockIdx.x < G ? total * (blockIdx.x + 1) / G : 0;
-  auto place = [&](int64_t T, int b) {  // tile T, in sequence b or a later one
+  // G CTAs with a share each, none of it empty (the count of a split unit's CTAs
+  // relies on that): CTA i has `each` tiles from i * each + min(i, more) on, and
+  // one more if i < more
+  const int total = start[a.nb], G = min((int)gridDim.x, total), me = blockIdx.x;
+  const int each = total / G, more = total - each * G;
+  if (me >= G) return;
+  const int t0 = me * each + min(me, more), t1 = t0 + each + (me < more);
+  auto owner = [&](int T) {  // the CTA whose share holds tile T
+    const int big = more * (each + 1);
+    return T < big ? T / (each + 1) : more + (T - big) / each;
+  };
+  auto place = [&](int T, int b) {  // tile T, in sequence b or a later one
     while (T >= start[b + 1]) ++b;
     KaPlace p;
     p.b = b;
-    p.n = (int)((start[b + 1] - start[b]) / units);
-    const int64_t rem = T - start[b];
-    const int u = (int)(rem / p.n);
-    p.j = (int)(rem - (int64_t)u * p.n);
+    p.n = (start[b + 1] - start[b]) / units;
+    const int rem = T - start[b], u = rem / p.n;
+    p.j = rem - u * p.n;
     p.kvh = u / a.n_tiles;
     p.tile = u - p.kvh * a.n_tiles;
     return p;
   };
-  auto locate = [&](int64_t T) {
+  auto locate = [&](int T) {
     int lo = 0, hi = a.nb - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
@@ -372,40 +401,46 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
   // this lane's bytes in a group: of the keys positions tok and tok + 2, of the values 4 dimensions of 4 positions
   const int k_at = (4 * (g >> 1) + (g & 1)) * 64 + t * 16, v_at = lane * 16;
 
-  int b_at = 0;
-  for (int64_t T = t0; T < t1;) {
-    const KaPlace p = T == t0 ? locate(T) : place(T, b_at);
-    b_at = p.b;
+  Kv8Warp<FMT, DIM, NT> w;
+  uint4 kf[DIM / 32], vf[DIM / 32];
+  float ks = 0.0f, vs = 0.0f;
+  KaPlace p = locate(t0);
+  Kv8Span s;
+  const uint8_t *kp, *vp;
+  const float *ka, *va;
+  int p0;
+  auto load_k = [&]() {
+#pragma unroll
+    for (int h = 0; h < DIM / 64; ++h) {
+      kf[2 * h] = ka_ld(kp + h * 1024);
+      kf[2 * h + 1] = ka_ld(kp + h * 1024 + 128);
+    }
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int j = 0; j < DIM / 32; ++j) vf[j] = ka_ld(vp + j * 512);
+  };
+  auto enter = [&]() {  // a unit's share: request its query rows, then its first tile
     const int4 sp = span[p.b];
-    const Kv8Span s{sp.z, sp.x, sp.y, sp.w};
-    const int64_t seg0 = T - p.j, seg1 = seg0 + p.n;  // the unit's tiles
-    const int n = (int)(min(seg1, t1) - T);           // those of this CTA
-    int p0 = s.lo / kKv8Group * kKv8Group + p.j * kTile + warp * kKv8Group;
+    s = Kv8Span{sp.z, sp.x, sp.y, sp.w};
+    w.load(a, a.b0 + p.b, p.kvh, p.tile, s.n * group, lane);
+    p0 = s.lo / kKv8Group * kKv8Group + p.j * kTile + warp * kKv8Group;
     const size_t head = (size_t)(a.b0 + p.b) * a.c.n_kv + p.kvh;
-    const uint8_t* kp = a.c.k + (head * a.c.L_max + p0) * DIM + k_at;
-    const uint8_t* vp = a.c.v + (head * a.c.L_max + p0) * DIM + v_at;
-    const float *ka = a.c.k_amax + head * blocks, *va = a.c.v_amax + head * blocks;
-    uint4 kf[DIM / 32], vf[DIM / 32];
-    float ks = 0.0f, vs = 0.0f;
-    auto load_k = [&]() {
-#pragma unroll
-      for (int h = 0; h < DIM / 64; ++h) {
-        kf[2 * h] = ka_ld(kp + h * 1024);
-        kf[2 * h + 1] = ka_ld(kp + h * 1024 + 128);
-      }
-    };
-    auto load_v = [&]() {
-#pragma unroll
-      for (int j = 0; j < DIM / 32; ++j) vf[j] = ka_ld(vp + j * 512);
-    };
+    kp = a.c.k + (head * a.c.L_max + p0) * DIM + k_at;
+    vp = a.c.v + (head * a.c.L_max + p0) * DIM + v_at;
+    ka = a.c.k_amax + head * blocks, va = a.c.v_amax + head * blocks;
     if (p0 < s.hi) {
-      load_k();
-      load_v();
       ks = ka[p0 >> a.block_log2];
       vs = va[p0 >> a.block_log2];
+      load_k();
+      load_v();
     }
-    Kv8Warp<FMT, DIM, NT> w;
-    w.init(a, a.b0 + p.b, p.kvh, p.tile, s, lane);
+  };
+  enter();
+  for (int T = t0; T < t1;) {
+    const int seg0 = T - p.j, seg1 = seg0 + p.n;  // the unit's tiles
+    const int n = min(seg1, t1) - T;              // those of this CTA
+    w.begin(a, p.tile, s, lane);
     for (int i = 0; i < n && p0 < s.hi; ++i) {
       const bool more = i + 1 < n && p0 + kTile < s.hi;
       float z[NT][4];
@@ -427,96 +462,107 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
       p0 += kTile;
     }
     T += n;
-    const bool ends = T == seg1;
-          // ---- merge the warps
-          const float back = w.top_v / (kv8_q<FMT>() * kKaLift);
+    const bool whole = seg0 >= t0 && T == seg1;
+    const KaPlace done = p;
+    const int n_q = s.n * group;
+    if (T < t1) {  // the next unit's data travels while this one's warps are merged
+      p = place(T, p.b);
+      enter();
+    }
+    // ---- merge the warps
+    const float back = w.top_v / (kv8_q<FMT>() * kKaLift);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = nt * 8 + 2 * t + e;
-              float l = w.l[nt][e];
-              l += __shfl_xor_sync(0xffffffffu, l, 4);
-              l += __shfl_xor_sync(0xffffffffu, l, 8);
-              l += __shfl_xor_sync(0xffffffffu, l, 16);
-              if (g == 0) {
-                wm[warp * 8 * NT + r] = w.m[nt][e];
-                wl[warp * 8 * NT + r] = l;
-              }
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * t + e;
+        float l = w.l[nt][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (g == 0) {
+          wm[warp * 8 * NT + r] = w.m[nt][e];
+          wl[warp * 8 * NT + r] = l;
+        }
 #pragma unroll
-              for (int j = 0; j < DIM / 32; ++j)
-                *reinterpret_cast<float4*>(wo + (warp * 8 * NT + r) * kRowW + 4 * (g + 8 * j)) =
-                    make_float4(w.o[nt][j][0][e] * back, w.o[nt][j][0][2 + e] * back, w.o[nt][j][1][e] * back,
-                                w.o[nt][j][1][2 + e] * back);
-            }
-          __syncthreads();
-          const bool whole = seg0 >= t0 && ends;
-          float* slot = a.part + (size_t)(2 * blockIdx.x + (seg0 < t0 ? 0 : 1)) * (8 * NT) * (DIM + 2);
-          const int n_q = s.n * group;
-          auto store = [&](int r, int d, float4 v) {  // row r of the tile: o of its query row and head
-            const int rr = p.tile * 8 * NT + r;
-            if (rr >= a.rows * group) return;
-            const int i = rr / group, h = p.kvh * group + rr - i * group;
-            if (rr >= n_q) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
-            *reinterpret_cast<uint2*>(a.o + ((int64_t)(a.b0 + p.b) * a.rows + i) * a.o_stride + h * DIM + d) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-          };
-          for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
-            const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
-            float mm = -INFINITY, ls = 0.0f;
+        for (int j = 0; j < DIM / 32; ++j)
+          *reinterpret_cast<float4*>(wo + (warp * 8 * NT + r) * kRowW + 4 * (g + 8 * j)) =
+              make_float4(w.o[nt][j][0][e] * back, w.o[nt][j][0][2 + e] * back, w.o[nt][j][1][e] * back,
+                          w.o[nt][j][1][2 + e] * back);
+      }
+    __syncthreads();
+    float* slot = a.part + (size_t)(2 * me + (seg0 < t0 ? 0 : 1)) * (8 * NT) * (DIM + 2);
+    for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
+      const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
+      float mm = -INFINITY, ls = 0.0f;
 #pragma unroll
-            for (int k = 0; k < W; ++k) mm = fmaxf(mm, wm[k * 8 * NT + r]);
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (mm > -INFINITY) {
+      for (int k = 0; k < W; ++k) mm = fmaxf(mm, wm[k * 8 * NT + r]);
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (mm > -INFINITY) {
 #pragma unroll
-              for (int k = 0; k < W; ++k) {
-                const float f = ex2(wm[k * 8 * NT + r] - mm);
-                const float4 v = *reinterpret_cast<const float4*>(wo + (k * 8 * NT + r) * kRowW + d);
-                ls += wl[k * 8 * NT + r] * f;
-                acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
-              }
-            }
-            if (whole) {
-              const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
-              store(r, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-            } else {
-              *reinterpret_cast<float2*>(slot + r * (DIM + 2) + d) = make_float2(acc.x, acc.y);
-              *reinterpret_cast<float2*>(slot + r * (DIM + 2) + d + 2) = make_float2(acc.z, acc.w);
-              if (d == 0) *reinterpret_cast<float2*>(slot + r * (DIM + 2) + DIM) = make_float2(mm, ls);
-            }
-          }
-          if (!whole) {
-            // the unit's CTAs: those whose shares hold its first and its last tile
-            const int64_t c0 = ((seg0 + 1) * G - 1) / total, c1 = (seg1 * G - 1) / total;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) last_s = atomicAdd(a.arrived + c0, 1u) == (uint32_t)(c1 - c0);
-            __syncthreads();
-            if (last_s) {
-              __threadfence();
-              for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
-                const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
-                float mm = -INFINITY, ls = 0.0f;
-                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int64_t c = c0; c <= c1; ++c) {
-                  const float* x = a.part + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * (8 * NT) + r) * (DIM + 2);
-                  const float2 ml = __ldcg(reinterpret_cast<const float2*>(x + DIM));
-                  const float2 v0 = __ldcg(reinterpret_cast<const float2*>(x + d)), v1 = __ldcg(reinterpret_cast<const float2*>(x + d + 2));
-                  if (ml.x == -INFINITY) continue;
-                  const float now = fmaxf(mm, ml.x), f = ex2(mm - now), h = ex2(ml.x - now);
-                  mm = now;
-                  ls = ls * f + ml.y * h;
-                  acc.x = acc.x * f + v0.x * h, acc.y = acc.y * f + v0.y * h;
-                  acc.z = acc.z * f + v1.x * h, acc.w = acc.w * f + v1.y * h;
-                }
-                const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
-                store(r, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-              }
-              if (tid == 0) atomicExch(a.arrived + c0, 0u);
-            }
-          }
-          __syncthreads();  // the merge buffers are free again
+        for (int k = 0; k < W; ++k) {
+          const float f = ex2(wm[k * 8 * NT + r] - mm);
+          const float4 v = *reinterpret_cast<const float4*>(wo + (k * 8 * NT + r) * kRowW + d);
+          ls += wl[k * 8 * NT + r] * f;
+          acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+        }
+      }
+      if (whole) {
+        ka_store<DIM, NT>(a, done, n_q, r, d, acc, ls);
+      } else {
+        *reinterpret_cast<float2*>(slot + r * (DIM + 2) + d) = make_float2(acc.x, acc.y);
+        *reinterpret_cast<float2*>(slot + r * (DIM + 2) + d + 2) = make_float2(acc.z, acc.w);
+        if (d == 0) *reinterpret_cast<float2*>(slot + r * (DIM + 2) + DIM) = make_float2(mm, ls);
+      }
+    }
+    __syncthreads();  // the merge buffers are free again
+  }
+
+  // ---- units that lie in other CTAs' shares too: the one of this share's first
+  // tile, and the one of its last. Whoever is the last of a unit's CTAs to get
+  // here joins its partials. (At the share's end, both counters at once, so that no
+  // unit's turn waits for a round trip.)
+  if (warp < 2 && lane == 0) {
+    const int T = warp == 0 ? t0 : t1 - 1;
+    const KaPlace e = locate(T);
+    const int seg0 = T - e.j, seg1 = seg0 + e.n;
+    int last = 0;
+    if (warp == 0 ? seg0 < t0 : seg0 >= t0 && seg1 > t1) {
+      const int c0 = owner(seg0), c1 = owner(seg1 - 1);
+      // (releases the partials of the whole CTA, written before the barrier above; acquires the others')
+      last = atomic_add_acq_rel(a.arrived + c0, 1u) == (uint32_t)(c1 - c0);
+    }
+    last_s[warp] = last;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    if (!last_s[side]) continue;
+    const int T = side == 0 ? t0 : t1 - 1;
+    const KaPlace e = locate(T);
+    const int c0 = owner(T - e.j), c1 = owner(T - e.j + e.n - 1);
+    {
+      const int n_q = span[e.b].w * group;
+      for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
+        const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
+        float mm = -INFINITY, ls = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+          const float* x = a.part + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * (8 * NT) + r) * (DIM + 2);
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(x + DIM));
+          const float2 v0 = __ldcg(reinterpret_cast<const float2*>(x + d)), v1 = __ldcg(reinterpret_cast<const float2*>(x + d + 2));
+          const float now = fmaxf(mm, ml.x), base = now > -INFINITY ? now : 0.0f;
+          const float f = ex2(mm - base), h = ex2(ml.x - base);
+          mm = now;
+          ls = ls * f + ml.y * h;
+          acc.x = acc.x * f + v0.x * h, acc.y = acc.y * f + v0.y * h;
+          acc.z = acc.z * f + v1.x * h, acc.w = acc.w * f + v1.y * h;
+        }
+        ka_store<DIM, NT>(a, e, n_q, r, d, acc, ls);
+      }
+      if (tid == 0) atomicExch(a.arrived + c0, 0u);
+    }
   }
 }
 

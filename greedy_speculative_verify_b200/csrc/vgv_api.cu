@@ -1379,8 +1379,11 @@ vg_status kv8_attn_launch(DevState* dev, const vg_kv8* c, int32_t rows, int32_t 
   a.arrived = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.arrived);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.o_stride = o_stride;
-  for (a.b0 = 0; a.b0 < c->B; a.b0 += kKaTable) {
-    a.nb = min(kKaTable, c->B - a.b0);
+  // sequences per launch: what the kernel's table holds, and no more than 2^30 tiles
+  const int64_t tiles = (int64_t)c->n_kv * a.n_tiles * (cdiv(c->L_max, kKv8Group * ka_warps(nt)) + 1);
+  const int per = (int)max((int64_t)1, min((int64_t)kKaTable, ((int64_t)1 << 30) / tiles));
+  for (a.b0 = 0; a.b0 < c->B; a.b0 += per) {
+    a.nb = min(per, c->B - a.b0);
     const int grid = min(dev->sms * ka_ctas(nt), kKaMaxGrid), threads = 32 * ka_warps(nt);
     ProfScope ps(VG_KERNEL_ATTENTION, s);
     const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
