@@ -154,7 +154,8 @@ struct Kv8Warp {
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       sum *= kKaTiny * 128.0f;
-      const float back = a.scale_log2 / up0 / up1 * (FMT == kKv8Int8 ? 1.0f / kKaTiny : 1.0f);
+      const float down0 = __int_as_float((127 - lift / 2) << 23), down1 = __int_as_float((127 - (lift - lift / 2)) << 23);
+      const float back = a.scale_log2 * down0 * down1 * (FMT == kKv8Int8 ? 1.0f / kKaTiny : 1.0f);
       const int r = (tile * NT + nt) * 8 + g, seen = r < n_q ? s.L + r / group : -1;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -334,6 +335,8 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
   __shared__ int4 span[kKaTable];          // lo, hi, L, n
   __shared__ int sums[kKaTable / 32];
   __shared__ int last_s[2];
+  __shared__ int ends[2][2];   // their first and last CTA
+  __shared__ KaPlace edge[2];  // the units of this share's first and last tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.n_heads / a.c.n_kv, units = a.c.n_kv * a.n_tiles;  // units per sequence
   griddep_launch_dependents();
@@ -464,12 +467,12 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
     T += n;
     const bool whole = seg0 >= t0 && T == seg1;
     const KaPlace done = p;
-    const int n_q = s.n * group;
-    if (T < t1) {  // the next unit's data travels while this one's warps are merged
-      p = place(T, p.b);
-      enter();
+    if (tid == 0) {
+      if (T - n == t0) edge[0] = p;
+      if (T == t1) edge[1] = p;
     }
-    // ---- merge the warps
+    const int n_q = s.n * group;
+    // ---- merge the warps: their sums to shared memory
     const float back = w.top_v / (kv8_q<FMT>() * kKaLift);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -490,6 +493,10 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
               make_float4(w.o[nt][j][0][e] * back, w.o[nt][j][0][2 + e] * back, w.o[nt][j][1][e] * back,
                           w.o[nt][j][1][2 + e] * back);
       }
+    if (T < t1) {  // the next unit's data travels while this one's warps are merged
+      p = place(T, p.b);
+      enter();
+    }
     __syncthreads();
     float* slot = a.part + (size_t)(2 * me + (seg0 < t0 ? 0 : 1)) * (8 * NT) * (DIM + 2);
     for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
@@ -523,12 +530,11 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
   // here joins its partials. (At the share's end, both counters at once, so that no
   // unit's turn waits for a round trip.)
   if (warp < 2 && lane == 0) {
-    const int T = warp == 0 ? t0 : t1 - 1;
-    const KaPlace e = locate(T);
-    const int seg0 = T - e.j, seg1 = seg0 + e.n;
+    const int seg0 = start[edge[warp].b] + (edge[warp].kvh * a.n_tiles + edge[warp].tile) * edge[warp].n, seg1 = seg0 + edge[warp].n;
     int last = 0;
     if (warp == 0 ? seg0 < t0 : seg0 >= t0 && seg1 > t1) {
       const int c0 = owner(seg0), c1 = owner(seg1 - 1);
+      ends[warp][0] = c0, ends[warp][1] = c1;
       // (releases the partials of the whole CTA, written before the barrier above; acquires the others')
       last = atomic_add_acq_rel(a.arrived + c0, 1u) == (uint32_t)(c1 - c0);
     }
@@ -538,9 +544,8 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
     if (!last_s[side]) continue;
-    const int T = side == 0 ? t0 : t1 - 1;
-    const KaPlace e = locate(T);
-    const int c0 = owner(T - e.j), c1 = owner(T - e.j + e.n - 1);
+    const KaPlace e = edge[side];
+    const int c0 = ends[side][0], c1 = ends[side][1];
     {
       const int n_q = span[e.b].w * group;
       for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
