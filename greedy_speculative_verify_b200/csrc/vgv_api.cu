@@ -1350,6 +1350,7 @@ vg_status kv8_append_launch(const vg_kv8* c, int32_t rows, const void* k, int64_
   const int grid = c->B * c->n_kv * a.nb * 2, units = c->block * c->dim / 16;
   const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
     constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
+    if (rows <= kKv8Few) return launch_dep(kv8_append_few<F, D>, c->B * c->n_kv, 128, 0, s, Launch::kPlain, a);
     if (units <= 256) return launch_dep(kv8_append<F, D, 1>, grid, units, 0, s, Launch::kPlain, a);
     if (units <= 512) return launch_dep(kv8_append<F, D, 2>, grid, 256, 0, s, Launch::kPlain, a);
     return launch_dep(kv8_append<F, D, 4>, grid, 256, 0, s, Launch::kPlain, a);
@@ -1438,22 +1439,23 @@ extern "C" vg_status vg_kv8_read(const vg_kv8* c, int32_t rows, const int32_t* p
   Kv8ReadArgs a{};
   a.c = kv8_view(c);
   a.rows = rows;
-  a.ng = (rows + kKv8Group - 2) / kKv8Group + 1;
+  a.ng = cdiv((rows + kKv8Group - 2) / kKv8Group + 1, kKv8ReadGroups);
   a.pos = pos;
   a.n_rows = n_rows;
   a.k_out = k_out;
   a.v_out = v_out;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
-  const int64_t threads = (int64_t)c->B * c->n_kv * a.ng * c->dim, grid = (threads + 255) / 256;
+  a.sides = k_out && v_out ? 2 : 1;
+  const int64_t grid = (int64_t)c->B * c->n_kv * a.ng * a.sides;
   if (grid >= ((int64_t)1 << 31)) return VG_ERR_UNSUPPORTED;
   DevState* dev = nullptr;
   if ((st = device_state(&dev)) != VG_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
     constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
-    return out_type == VG_F32 ? launch_dep(kv8_read<F, D, float>, (int)grid, 256, 0, s, Launch::kPlain, a)
-                              : launch_dep(kv8_read<F, D, __nv_bfloat16>, (int)grid, 256, 0, s, Launch::kPlain, a);
+    return out_type == VG_F32 ? launch_dep(kv8_read<F, D, float>, (int)grid, kKv8ReadThreads, 0, s, Launch::kPlain, a)
+                              : launch_dep(kv8_read<F, D, __nv_bfloat16>, (int)grid, kKv8ReadThreads, 0, s, Launch::kPlain, a);
   });
   return e == cudaSuccess ? VG_OK : cuda_fail();
 }

@@ -107,6 +107,21 @@ def test_append(fmt, dim, block, n_kv):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_append_few_rows(fmt, dim):
+    """One to nine rows (a verify step takes a path of its own) from every
+    position of a group of 16, over block ends, magnitudes growing and not."""
+    c = Cache(fmt, 16, 2, 128, dim, 32, seed=31)
+    for rows in range(1, 10):
+        for at in (0, 16, 48, 128 - 15 - rows):
+            size = float(c.g.choice([0.1, 3.0]))
+            x = {y: oracle.widen(oracle.round_bf16_bits(c.g.normal(0, size, (16, rows, 2, dim)))) for y in "kv"}
+            c.append(rows, [at + b for b in range(16)], [min(rows, 1 + (b + at) % 9) for b in range(16)], x=x)
+    ok()
+    c.check()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_append_rounds_ties_to_even(fmt):
     """Rows whose quotients by the magnitude are exact ties (x Q / a = k + 1/2, in
     e4m3 halfway between neighbours), for several magnitudes, and earlier codes
