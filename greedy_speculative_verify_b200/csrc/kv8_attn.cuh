@@ -43,7 +43,6 @@ struct Kv8AttnArgs {
   Kv8View c;
   int32_t b0, nb;                // the launch's sequences: b0 .. b0 + nb - 1
   int32_t rows, n_heads, n_tiles;  // rows per sequence; n_tiles: 8 NT-row tiles of a kv head's rows * group query rows
-  int32_t block_log2;
   const __nv_bfloat16* q;
   int64_t q_stride;
   const int32_t* lens;   // [B] positions before the new rows
@@ -399,7 +398,7 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
     }
     return place(T, lo);
   };
-  const size_t blocks = (size_t)a.c.L_max >> a.block_log2;
+  const size_t blocks = (size_t)a.c.L_max >> a.c.log2;
   const int g = lane >> 2, t = lane & 3;
   // this lane's bytes in a group: of the keys positions tok and tok + 2, of the values 4 dimensions of 4 positions
   const int k_at = (4 * (g >> 1) + (g & 1)) * 64 + t * 16, v_at = lane * 16;
@@ -433,8 +432,8 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
     vp = a.c.v + (head * a.c.L_max + p0) * DIM + v_at;
     ka = a.c.k_amax + head * blocks, va = a.c.v_amax + head * blocks;
     if (p0 < s.hi) {
-      ks = ka[p0 >> a.block_log2];
-      vs = va[p0 >> a.block_log2];
+      ks = ka[p0 >> a.c.log2];
+      vs = va[p0 >> a.c.log2];
       load_k();
       load_v();
     }
@@ -453,8 +452,8 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
       if (more) {
         kp += kTile * DIM;
         load_k();
-        ks = ka[(p0 + kTile) >> a.block_log2];
-        vs = va[(p0 + kTile) >> a.block_log2];
+        ks = ka[(p0 + kTile) >> a.c.log2];
+        vs = va[(p0 + kTile) >> a.c.log2];
       }
       w.weights(z, ks_now, vs_now, p0, s.lo, p0 >= s.lo && p0 + kKv8Group - 1 <= s.L, lane, b0, b1);
       w.values(vf, b0, b1, s.hi - p0, lane);

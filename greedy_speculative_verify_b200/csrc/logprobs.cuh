@@ -349,7 +349,7 @@ struct LpFinishArgs {
   float* top_logprobs;    // [R, n_top]
 };
 
-constexpr int kLpFinishThreads = 256;
+constexpr int kLpFinishThreads = 512;
 constexpr int kLpMaxGroups = 512;
 constexpr int kLpFix = 12;  // candidates whose exact logits enter the sums: the same however many alternatives are asked for
 
@@ -359,7 +359,9 @@ constexpr int kLpFix = 12;  // candidates whose exact logits enter the sums: the
 // exact ones in the sums too: the tensor cores cut every partial sum towards
 // zero (about 1.5e-8 of a logit for each 16 products, 1.2e-6 at H = 1,280), which
 // shifts all logits alike but for their size, so where a few tokens hold the
-// mass, correcting those removes most of the error.
+// mass, correcting those removes most of the error. The kernel is a chain of round
+// trips (statistics and heads; the lists; the candidates' rows), each with all its
+// loads under way at once.
 template <int NC>
 __global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinishArgs a) {
   constexpr int NW = kLpFinishThreads / 32;
@@ -368,75 +370,77 @@ __global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinis
   __shared__ unsigned long long head[kLpMaxGroups], pool[NC * NC], best[NC];
   __shared__ unsigned long long floor_s;
   __shared__ int id_s[NC + 1], n_pool;
+  static_assert(kLpMaxGroups <= kLpFinishThreads, "one unit a thread");
   griddep_launch_dependents();
   griddep_wait();
   const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tok = a.tokens ? a.tokens[r] : -1;
   if (tid == 0) n_pool = 0, floor_s = 1ull;  // 0 keys are no candidates
   if (tid < NC) best[tid] = 0ull;
   // ---- the units' sums, rescaled to the common maximum
-  float m = -INFINITY;
-  for (int g = tid; g < a.n_groups; g += kLpFinishThreads) {
-    m = fmaxf(m, a.stat[(size_t)g * 3 * a.R + r]);
-    head[g] = a.cand[((size_t)g * a.R + r) * NC];
+  const bool mine = tid < a.n_groups;
+  float mg = -INFINITY, Sg = 0.0f, Tg = 0.0f;
+  unsigned long long first = 0ull;
+  if (mine) {
+    const float* st = a.stat + (size_t)tid * 3 * a.R + r;
+    mg = st[0], Sg = st[a.R], Tg = st[2 * (size_t)a.R];
+    first = a.cand[((size_t)tid * a.R + r) * NC];
+    head[tid] = first;
   }
+  float m = mg;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red_m[warp] = m;
   __syncthreads();
-  for (int w = 0; w < NW; ++w) m = fmaxf(m, red_m[w]);
-  double S = 0.0, T = 0.0;
-  for (int g = tid; g < a.n_groups; g += kLpFinishThreads) {
-    const float* st = a.stat + (size_t)g * 3 * a.R + r;
-    const float mg = st[0], Sg = st[a.R], Tg = st[2 * (size_t)a.R];
-    const double d = mg > -INFINITY ? (double)mg - (double)m : 0.0, f = mg > -INFINITY ? exp(d) : 1.0;
-    S += f * Sg;
-    T += f * (Tg + Sg * d);
-    int rank = 0;
-    const unsigned long long mine = head[g];
-    for (int k = 0; k < a.n_groups; ++k) rank += head[k] > mine;
-    if (rank == NC - 1 && mine) floor_s = mine;
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    S += __shfl_xor_sync(0xffffffffu, S, o);
-    T += __shfl_xor_sync(0xffffffffu, T, o);
-  }
-  if (lane == 0) red_s[warp] = S, red_t[warp] = T;
-  __syncthreads();
-  for (int g = tid; g < a.n_groups; g += kLpFinishThreads)
-    if (head[g] >= floor_s) {
-      const unsigned long long* l = a.cand + ((size_t)g * a.R + r) * NC;
-#pragma unroll 4
-      for (int k = 0; k < NC; ++k) {
-        const unsigned long long key = l[k];
-        if (key < floor_s) break;
-        pool[atomicAdd(&n_pool, 1)] = key;
-      }
+  for (int w = 0; w < NW; ++w) m = fmaxf(m, red_m[w]);
+  if (warp * 32 < a.n_groups) {  // whole warps
+    int rank = 0;
+#pragma unroll 8
+    for (int k = 0; k < a.n_groups; ++k) rank += head[k] > first;
+    if (rank == NC - 1 && first) floor_s = first;
+    // a unit's largest term is 1 before rescaling, so the factor needs fp32 accuracy only
+    const float d = mg > -INFINITY ? mg - m : 0.0f, f = mg > -INFINITY ? ex2(d * 1.4426950408889634f) : 1.0f;
+    double S = (double)f * Sg, T = mine ? (double)f * ((double)Tg + (double)Sg * fmaxf(d, -1000.0f)) : 0.0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      S += __shfl_xor_sync(0xffffffffu, S, o);
+      T += __shfl_xor_sync(0xffffffffu, T, o);
     }
+    if (lane == 0) red_s[warp] = S, red_t[warp] = T;
+  }
+  __syncthreads();
+  if (mine && first >= floor_s) {
+    const uint4* l = reinterpret_cast<const uint4*>(a.cand + ((size_t)tid * a.R + r) * NC);
+    uint4 x[NC / 2];
+#pragma unroll
+    for (int k = 0; k < NC / 2; ++k) x[k] = l[k];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const unsigned long long key = k & 1 ? (unsigned long long)x[k / 2].w << 32 | x[k / 2].z
+                                           : (unsigned long long)x[k / 2].y << 32 | x[k / 2].x;
+      if (key >= floor_s) pool[atomicAdd(&n_pool, 1)] = key;
+    }
+  }
   __syncthreads();
   for (int i = tid; i < n_pool; i += kLpFinishThreads) {
-    const unsigned long long mine = pool[i];
+    const unsigned long long key = pool[i];
     int rank = 0;
-    for (int k = 0; k < n_pool; ++k) rank += pool[k] > mine;
-    if (rank < NC) best[rank] = mine;
-  }
-  const int tok = a.tokens ? a.tokens[r] : -1;
-  __syncthreads();
-  if (tid < NC) id_s[tid] = best[tid] ? (int)(0xFFFFFFFFu - (uint32_t)(best[tid] & 0xFFFFFFFFull)) : -1;
-  if (tid == 0) {
-    id_s[NC] = tok >= 0 && tok < a.V ? tok : -1;
-    if (tok >= a.V) record_error(kErrBounds, 355);
+#pragma unroll 8
+    for (int k = 0; k < n_pool; ++k) rank += pool[k] > key;
+    if (rank < NC) best[rank] = key;
   }
   __syncthreads();
   // ---- their logits from exact products (a product of two bf16 is exact in fp32), summed in fp64
   for (int k = warp; k <= NC; k += NW) {
-    const int v = id_s[k];
+    const int v = k < NC ? (best[k] ? (int)(0xFFFFFFFFu - (uint32_t)(best[k] & 0xFFFFFFFFull)) : -1)
+                         : (tok >= 0 && tok < a.V ? tok : -1);
     double z = -INFINITY;
     if (v >= 0) {
       const uint4* x = reinterpret_cast<const uint4*>(a.h + (size_t)r * a.H);
       const uint4* w = reinterpret_cast<const uint4*>(a.lm + (size_t)v * a.H);
       double z0 = 0.0, z1 = 0.0, z2 = 0.0, z3 = 0.0;
-#pragma unroll 2
+#pragma unroll 5
       for (int i = lane; i < a.H / 8; i += 32) {
         const uint4 xv = x[i], wv = w[i];
         z0 += (double)(bf16_lo(xv.x) * bf16_lo(wv.x));
@@ -452,38 +456,42 @@ __global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinis
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     }
-    if (lane == 0) {
-      z_s[k] = z;
-      if (k < kLpFix) {  // what the exact logit changes in S and T
-        double ds = 0.0, dt = 0.0;
-        if (v >= 0 && m < INFINITY) {
-          const double d0 = (double)lp_unkey((uint32_t)(best[k] >> 32)) - (double)m, d1 = z - (double)m;
-          const double e0 = exp(d0), e1 = exp(d1);
-          ds = e1 - e0;
-          dt = e1 * d1 - e0 * d0;
-        }
-        s_fix[k] = ds, t_fix[k] = dt;
-      }
+    if (lane == 0) z_s[k] = z, id_s[k] = v;
+  }
+  if (tid == 0 && tok >= a.V) record_error(kErrBounds, 355);
+  __syncthreads();
+  if (tid < kLpFix) {  // what the exact logits change in S and T
+    double ds = 0.0, dt = 0.0;
+    if (id_s[tid] >= 0 && m < INFINITY) {
+      const double d0 = (double)lp_unkey((uint32_t)(best[tid] >> 32)) - (double)m, d1 = z_s[tid] - (double)m;
+      // e^d1 - e^d0 = e^d0 (e^(d1 - d0) - 1): d1 - d0 is a rounding's worth, and needs no more than fp32 accuracy
+      const double e0 = (double)expf((float)d0), g = d1 - d0, gain = (double)expm1f((float)g);
+      ds = e0 * gain;
+      dt = e0 * (g + gain * d1);
     }
+    s_fix[tid] = ds, t_fix[tid] = dt;
   }
   __syncthreads();
-  S = 0.0, T = 0.0;
-  for (int w = 0; w < NW; ++w) S += red_s[w], T += red_t[w];
+  if (warp != 0) return;
+  double S = 0.0, T = 0.0;
+  for (int w = 0; w * 32 < a.n_groups; ++w) S += red_s[w], T += red_t[w];
+#pragma unroll
   for (int k = 0; k < kLpFix; ++k) S += s_fix[k], T += t_fix[k];
   const double log_s = log(S), lse = (double)m + log_s;
-  if (tid == 0) {
+  if (lane == 0) {
     if (a.logprob) a.logprob[r] = (float)(z_s[NC] - lse);
     if (a.entropy) a.entropy[r] = (float)(log_s - T / S);
   }
   // ---- order: rank of each candidate by (logit, lower index first)
-  if (tid < NC) {
-    const double z = z_s[tid];
-    const int v = id_s[tid];
+  if (lane < NC) {
+    const double z = z_s[lane];
+    const int v = id_s[lane];
     int rank = 0;
+#pragma unroll
     for (int k = 0; k < NC; ++k) {
-      if (k == tid) continue;
+      if (k == lane) continue;
       // candidates that are missing (fewer logits above -inf than asked for) come last, in list order
-      const bool ahead = id_s[k] < 0 ? (v < 0 && k < tid) : (v < 0 || z_s[k] > z || (z_s[k] == z && id_s[k] < v));
+      const bool ahead = id_s[k] < 0 ? (v < 0 && k < lane) : (v < 0 || z_s[k] > z || (z_s[k] == z && id_s[k] < v));
       rank += ahead;
     }
     if (rank < a.n_top) {

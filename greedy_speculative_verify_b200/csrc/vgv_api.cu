@@ -1274,7 +1274,9 @@ bool kv8_overlaps(const vg_kv8* c, const void* p, size_t bytes) {
 }
 
 vg::Kv8View kv8_view(const vg_kv8* c) {
-  return vg::Kv8View{c->B,     c->L_max, c->n_kv, c->block, static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v),
+  int log2 = 4;
+  while ((1 << log2) < c->block) ++log2;
+  return vg::Kv8View{c->B, c->L_max, c->n_kv, c->block, log2, static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v),
                      c->k_amax, c->v_amax};
 }
 
@@ -1351,9 +1353,8 @@ vg_status kv8_append_launch(const vg_kv8* c, int32_t rows, const void* k, int64_
   const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
     constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
     if (rows <= kKv8Few) return launch_dep(kv8_append_few<F, D>, c->B * c->n_kv, 128, 0, s, Launch::kPlain, a);
-    if (units <= 256) return launch_dep(kv8_append<F, D, 1>, grid, units, 0, s, Launch::kPlain, a);
-    if (units <= 512) return launch_dep(kv8_append<F, D, 2>, grid, 256, 0, s, Launch::kPlain, a);
-    return launch_dep(kv8_append<F, D, 4>, grid, 256, 0, s, Launch::kPlain, a);
+    if (units < 128) return launch_dep(kv8_append<F, D, 2>, grid, units / 2, 0, s, Launch::kPlain, a);
+    return launch_dep(kv8_append<F, D, 4>, grid, units / 4, 0, s, Launch::kPlain, a);
   });
   return e == cudaSuccess ? VG_OK : cuda_fail();
 }
@@ -1369,7 +1370,6 @@ vg_status kv8_attn_launch(DevState* dev, const vg_kv8* c, int32_t rows, int32_t 
   a.rows = rows;
   a.n_heads = n_heads;
   a.n_tiles = cdiv(rows * group, 8 * nt);
-  for (a.block_log2 = 4; (1 << a.block_log2) < c->block;) ++a.block_log2;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
   a.lens = lens;
