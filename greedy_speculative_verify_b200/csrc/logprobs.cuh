@@ -6,7 +6,8 @@
 //
 // logprob_tiles: tcgen05 GEMM with 128 rows of h as M and a tile of vocabulary
 // rows as N; a unit of work is a group of consecutive vocabulary tiles for one
-// 128-row block. The epilogue thread that owns a row reads its logits from
+// 128-row block (PAIR: for 256 rows, by two CTAs that share the vocabulary tile:
+// cta_group::2). The epilogue thread that owns a row reads its logits from
 // tensor memory and keeps, in one pass, the running maximum m, S = sum e^(z-m),
 // T = sum e^(z-m) (z-m), and the candidates: the largest logits, at least kLpSpare more than
 // the n asked for.
@@ -39,9 +40,10 @@ struct LpArgs {
   uint32_t* floor;             // [R] or null: order-preserving image of a logit that NC others reach (0: none known)
 };
 
-__host__ __device__ constexpr int lp_stage_bytes(int tile_n) { return kLpABytes + tile_n * kBK * 2; }
-__host__ __device__ constexpr int lp_smem_bytes(int tile_n, int stages) {
-  return 1024 + stages * lp_stage_bytes(tile_n) + kLpAux + kLpPend * kLpM * 8;
+// b_rows: vocabulary rows of a tile that one CTA holds
+__host__ __device__ constexpr int lp_stage_bytes(int b_rows) { return kLpABytes + b_rows * kBK * 2; }
+__host__ __device__ constexpr int lp_smem_bytes(int b_rows, int stages) {
+  return 1024 + stages * lp_stage_bytes(b_rows) + kLpAux + kLpPend * kLpM * 8;
 }
 
 // Candidates kept for n alternatives: n + kLpSpare rounded up to a size the
@@ -77,13 +79,22 @@ __device__ __forceinline__ float lp_unkey(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
 }
 
-template <int NC>
+// PAIR: the two CTAs of a cluster take row blocks 2 i and 2 i + 1; each loads its
+// own rows of h and its half of the vocabulary tile into its own shared memory and
+// epilogues its own rows. All loads of a stage complete on the even CTA's barrier,
+// which expects both CTAs' bytes; the even CTA issues the MMAs. (The odd CTA
+// watching its own stages and passing them on took 1,920 us for 4,096 rows, against
+// @@ us: a round trip more than six stages cover.) Shared memory then
+// carries 64 + 64 instead of 96 + 96 bytes a cycle at full tensor rate, operands read
+// and tiles written, against the 128 it has.
+template <int NC, bool PAIR>
 __global__ void __launch_bounds__(192, 1)
     logprob_tiles(const __grid_constant__ CUtensorMap mapH, const __grid_constant__ CUtensorMap mapLM, const LpArgs a) {
   constexpr int kMaxStages = 8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int stages = a.stages, stage_bytes = lp_stage_bytes(a.tile_n);
+  const int b_rows = PAIR ? a.tile_n / 2 : a.tile_n;
+  const int stages = a.stages, stage_bytes = lp_stage_bytes(b_rows);
   uint8_t* aux = tiles + stages * stage_bytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(aux);
   uint64_t* empty = full + kMaxStages;
@@ -95,7 +106,11 @@ __global__ void __launch_bounds__(192, 1)
   float2* pend = reinterpret_cast<float2*>(aux + kLpAux);  // [kLpPend][kLpM]: (logit, column) waiting
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int total = a.n_groups * a.n_mblk;  // unit = (vocabulary group, row block), row block fastest
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int n_rb = PAIR ? cdiv(a.n_mblk, 2) : a.n_mblk;
+  const int total = a.n_groups * n_rb;  // unit = (vocabulary group, row block or pair of them), rows fastest
+  const int unit0 = PAIR ? blockIdx.x / 2 : blockIdx.x, unit_step = PAIR ? gridDim.x / 2 : gridDim.x;
+  const int b_row0 = rank * b_rows;  // this CTA's share of a vocabulary tile
   const uint32_t a_bytes = a.a_box_rows * kBK * 2, b_bytes = a.b_box_rows * kBK * 2;
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
@@ -105,7 +120,7 @@ __global__ void __launch_bounds__(192, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 4);
+      mbar_init(&tempty[i], PAIR ? 8 : 4);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -114,11 +129,17 @@ __global__ void __launch_bounds__(192, 1)
     prefetch_tmap(&mapLM);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t limit = g_wait_timeout_ns;
@@ -126,13 +147,18 @@ __global__ void __launch_bounds__(192, 1)
   // vocabulary tiles of the first stages before the dependency wait: the LM head is immutable
   int npre = 0;
   const uint64_t pol_w = a.n_mblk == 1 ? policy_evict_first() : policy_evict_normal();
-  if (warp == 0 && lane == 0 && (int)blockIdx.x < total) {
-    const int g = blockIdx.x / a.n_mblk;
+  if (warp == 0 && lane == 0 && unit0 < total) {
+    const int g = unit0 / n_rb;
     const int vb1 = min(a.n_vblk, (g + 1) * a.group_tiles);
     for (int vb = g * a.group_tiles; vb < vb1 && npre < stages; ++vb)
       for (int kc = 0; kc < a.k_chunks && npre < stages; ++kc, ++npre) {
-        mbar_expect_tx(&full[npre], b_bytes);
-        tma_load_2d_hint(tiles + npre * stage_bytes + kLpABytes, &mapLM, &full[npre], kc * kBK, vb * a.tile_n, pol_w);
+        uint8_t* dst = tiles + npre * stage_bytes + kLpABytes;
+        if (PAIR) {  // (expected with the stage's arrival: bytes may land before)
+          tma_load_2d_pair(dst, &mapLM, &full[npre], kc * kBK, vb * a.tile_n + b_row0, pol_w);
+        } else {
+          mbar_expect_tx(&full[npre], b_bytes);
+          tma_load_2d_hint(dst, &mapLM, &full[npre], kc * kBK, vb * a.tile_n, pol_w);
+        }
       }
   }
   griddep_wait();
@@ -142,8 +168,8 @@ __global__ void __launch_bounds__(192, 1)
       const uint64_t pol_h = policy_evict_last();
       int stage = 0, it = 0;
       uint32_t phase = 0, issued = 0, last_par = 0;
-      for (int u = blockIdx.x; u < total && !*abort_flag; u += gridDim.x) {
-        const int g = u / a.n_mblk, mb = u - g * a.n_mblk;
+      for (int u = unit0; u < total && !*abort_flag; u += unit_step) {
+        const int g = u / n_rb, mb = PAIR ? 2 * (u - g * n_rb) + rank : u - g * n_rb;
         const int vb1 = min(a.n_vblk, (g + 1) * a.group_tiles);
         for (int vb = g * a.group_tiles; vb < vb1 && !*abort_flag; ++vb) {
           for (int kc = 0; kc < a.k_chunks; ++kc, ++it) {
@@ -154,9 +180,15 @@ __global__ void __launch_bounds__(192, 1)
             }
             uint8_t* st = tiles + stage * stage_bytes;
             const bool pre = it < npre;  // its vocabulary tile is already in flight
-            mbar_arrive_expect_tx(&full[stage], pre ? a_bytes : a_bytes + b_bytes);
-            tma_load_2d_hint(st, &mapH, &full[stage], kc * kBK, mb * kLpM, pol_h);
-            if (!pre) tma_load_2d_hint(st + kLpABytes, &mapLM, &full[stage], kc * kBK, vb * a.tile_n, pol_w);
+            if (PAIR) {
+              if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (a_bytes + b_bytes));
+              tma_load_2d_pair(st, &mapH, &full[stage], kc * kBK, mb * kLpM, pol_h);
+              if (!pre) tma_load_2d_pair(st + kLpABytes, &mapLM, &full[stage], kc * kBK, vb * a.tile_n + b_row0, pol_w);
+            } else {
+              mbar_arrive_expect_tx(&full[stage], pre ? a_bytes : a_bytes + b_bytes);
+              tma_load_2d_hint(st, &mapH, &full[stage], kc * kBK, mb * kLpM, pol_h);
+              if (!pre) tma_load_2d_hint(st + kLpABytes, &mapLM, &full[stage], kc * kBK, vb * a.tile_n, pol_w);
+            }
             issued |= 1u << stage;
             last_par = (last_par & ~(1u << stage)) | (phase << stage);
             if (++stage == stages) {
@@ -169,27 +201,31 @@ __global__ void __launch_bounds__(192, 1)
       // stages armed before the wait but never reached (an abort): arrive, so
       // their copies complete the phase and can be drained below
       for (; it < npre; ++it) {
-        mbar_arrive(&full[it]);
+        if (PAIR && rank == 0) mbar_arrive_expect_tx(&full[it], 2 * b_bytes);
+        if (!PAIR) mbar_arrive(&full[it]);
         issued |= 1u << it;
         last_par &= ~(1u << it);
       }
+      // (a pair's copies are all counted in the even CTA)
       for (int s = 0; s < stages; ++s)
-        if (issued & (1u << s)) mbar_wait(&full[s], (last_par >> s) & 1, limit);
+        if (rank == 0 && (issued & (1u << s))) mbar_wait(&full[s], (last_par >> s) & 1, limit);
     }
+  } else if (warp == 1 && PAIR && rank == 1) {  // the even CTA issues the pair's MMAs
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(kLpM, a.tile_n);
+      const uint32_t idesc = idesc_bf16_f32(PAIR ? 2 * kLpM : kLpM, a.tile_n);
       int stage = 0;
       uint32_t phase = 0;
       int lt = 0;  // local tile counter: selects the accumulator buffer
       bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const int g = u / a.n_mblk;
+      for (int u = unit0; u < total && ok; u += unit_step) {
+        const int g = u / n_rb;
         const int vb1 = min(a.n_vblk, (g + 1) * a.group_tiles);
         for (int vb = g * a.group_tiles; vb < vb1 && ok; ++vb, ++lt) {
           const int ab = lt & 1;
           const uint32_t ap = (lt >> 1) & 1;
-          if (*abort_flag || !mbar_wait(&tempty[ab], ap ^ 1, limit)) {
+          if (*abort_flag ||
+              !(PAIR ? mbar_wait_cluster(&tempty[ab], ap ^ 1, limit) : mbar_wait(&tempty[ab], ap ^ 1, limit))) {
             record_error(kErrTimeout, 352);
             *abort_flag = 1;
             ok = false;
@@ -208,18 +244,33 @@ __global__ void __launch_bounds__(192, 1)
             const uint32_t st = smem_u32(tiles + stage * stage_bytes);
             const uint64_t da = sw128_kmajor_desc(st), db = sw128_kmajor_desc(st + kLpABytes);
 #pragma unroll
-            for (int k16 = 0; k16 < kBK / 16; ++k16)
-              umma_bf16(d, da + 2 * k16, db + 2 * k16, idesc, (kc | k16) != 0);
-            umma_commit(&empty[stage]);
+            for (int k16 = 0; k16 < kBK / 16; ++k16) {
+              if (PAIR)
+                umma_bf16_pair(d, da + 2 * k16, db + 2 * k16, idesc, (kc | k16) != 0);
+              else
+                umma_bf16(d, da + 2 * k16, db + 2 * k16, idesc, (kc | k16) != 0);
+            }
+            if (PAIR)
+              umma_commit_pair(&empty[stage]);
+            else
+              umma_commit(&empty[stage]);
             if (++stage == stages) {
               stage = 0;
               phase ^= 1;
             }
           }
-          if (ok) umma_commit(&tfull[ab]);
+          if (ok) {
+            if (PAIR)
+              umma_commit_pair(&tfull[ab]);
+            else
+              umma_commit(&tfull[ab]);
+          }
         }
       }
-      umma_commit(mma_done);
+      if (PAIR)
+        umma_commit_pair(mma_done);
+      else
+        umma_commit(mma_done);
       mbar_wait(mma_done, 0, limit);
     }
   } else {
@@ -232,8 +283,8 @@ __global__ void __launch_bounds__(192, 1)
     int lt = 0;
     bool ok = true;
     LpList<NC> list;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      const int g = u / a.n_mblk, mb = u - g * a.n_mblk;
+    for (int u = unit0; u < total && ok; u += unit_step) {
+      const int g = u / n_rb, mb = PAIR ? 2 * (u - g * n_rb) + rank : u - g * n_rb;
       const int vb1 = min(a.n_vblk, (g + 1) * a.group_tiles);
       const int r = mb * kLpM + row;
       const bool busy = mb * kLpM + q * 32 < a.R;  // this warp has rows
@@ -313,7 +364,12 @@ __global__ void __launch_bounds__(192, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[ab]);
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_at(&tempty[ab], 0);
+          else
+            mbar_arrive(&tempty[ab]);
+        }
       }
       if (busy) settle();
       if (ok && r < a.R) {
@@ -330,9 +386,13 @@ __global__ void __launch_bounds__(192, 1)
     }
   }
   __syncthreads();
+  if (PAIR) cluster_sync();  // neither CTA's memory is read or signalled any more
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, 512);
+    else
+      tmem_dealloc(tmem_base, 512);
   }
 }
 

@@ -69,6 +69,7 @@ constexpr int kPreL2Chunks = VG_PRE_L2_CHUNKS;  // further k-chunks of the first
 struct DevState {
   bool init = false;
   int sms = 0;
+  int lp_pairs = 0;  // pairs of CTAs of the log-probability kernel that run at once
 };
 DevState g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -151,11 +152,26 @@ vg_status device_state(DevState** out) {
     if (cudaFuncSetAttribute(vg::lmhead_argmax_accept, cudaFuncAttributeMaxDynamicSharedMemorySize, vg::kLmSmemBytes) !=
         cudaSuccess)
       return cuda_fail();
-    for (auto* k : {vg::logprob_tiles<12>, vg::logprob_tiles<24>})
+    for (auto* k : {vg::logprob_tiles<12, false>, vg::logprob_tiles<24, false>, vg::logprob_tiles<12, true>,
+                    vg::logprob_tiles<24, true>})
       if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
               cudaSuccess)
         return cuda_fail();
+    {  // pairs of CTAs that fit the GPU at once
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(d.sms / 2 * 2);
+      cfg.blockDim = dim3(192);
+      cfg.dynamicSmemBytes = kMaxSmemBytes;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = 2;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&d.lp_pairs, vg::logprob_tiles<24, true>, &cfg) != cudaSuccess || d.lp_pairs < 1)
+        return cuda_fail();
+    }
     // Kernels that follow each other with dependent launches share SMs only if
     // their shared-memory configurations agree: every kernel of the decode
     // chain asks for the largest shared-memory carveout.
@@ -1574,7 +1590,8 @@ namespace {
 
 // How a call is cut: vocabulary tile, tiles per unit of work, candidates per unit.
 struct LpPlan {
-  int tile_n, stages, n_vblk, group_tiles, n_groups, n_mblk, n_cand;
+  bool pair;
+  int tile_n, b_rows, stages, n_vblk, group_tiles, n_groups, n_mblk, n_cand;
   size_t stat, cand, floor, total;
 };
 LpPlan lp_plan(int R, int V, int n_top) {
@@ -1583,19 +1600,35 @@ LpPlan lp_plan(int R, int V, int n_top) {
   LpPlan p{};
   p.n_cand = lp_cands(n_top);
   p.n_mblk = cdiv(R, kLpM);
-  if (p.n_mblk == 1) {
-    p.tile_n = 176;
-    p.group_tiles = 5;
-  } else {
+  // one row block: a stream of the LM head, one CTA per SM; more: the tensor
+  // cores bound, pairs of CTAs on 256 rows
+  p.pair = p.n_mblk > 1;
+  const int workers = p.pair ? kSms / 2 : kSms, n_rb = p.pair ? cdiv(p.n_mblk, 2) : 1;
+  // The busiest worker's columns, with 16 more a tile for filling the pipeline and
+  // 32 a unit for its lists, decide between the cuts. Pairs keep the largest tile.
+  int64_t best = -1;
+  for (int tile = 256; tile >= (p.pair ? 256 : 64); tile -= 16) {
+    const int n_vblk = cdiv(V, tile);
+    const int most = p.pair ? 16 : cdiv(n_vblk, kSms);
+    for (int g = p.pair ? 1 : most; g <= most; ++g) {
+      const int64_t units = (int64_t)cdiv(n_vblk, g) * n_rb;
+      const int64_t cost = (units + workers - 1) / workers * ((int64_t)min(g, n_vblk) * (tile + 16) + 32);
+      if (cdiv(n_vblk, g) <= kLpMaxGroups && (best < 0 || cost < best)) {
+        best = cost;
+        p.tile_n = tile;
+        p.group_tiles = g;
+      }
+    }
+  }
+  if (best < 0) {  // a vocabulary of more groups than the finishing kernel takes
     p.tile_n = 256;
-    p.group_tiles = 8;
+    p.group_tiles = cdiv(cdiv(V, 256), kLpMaxGroups);
   }
   p.n_vblk = cdiv(V, p.tile_n);
-  while (cdiv(p.n_vblk, p.group_tiles) > kLpMaxGroups) ++p.group_tiles;
-  p.stages = 5;
-  while (lp_smem_bytes(p.tile_n, p.stages) > kMaxSmemBytes) --p.stages;
   p.n_groups = cdiv(p.n_vblk, p.group_tiles);
-  (void)kSms;
+  p.b_rows = p.pair ? p.tile_n / 2 : p.tile_n;
+  p.stages = 8;
+  while (lp_smem_bytes(p.b_rows, p.stages) > kMaxSmemBytes) --p.stages;
   p.stat = 0;
   p.cand = align256((size_t)p.n_groups * 3 * R * 4);
   p.floor = p.cand + align256((size_t)p.n_groups * R * p.n_cand * 8);
@@ -1643,12 +1676,12 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
   a.group_tiles = p.group_tiles;
   a.n_groups = p.n_groups;
   a.a_box_rows = box_rows(R, kLpM);
-  a.b_box_rows = box_rows(V, p.tile_n);
+  a.b_box_rows = box_rows(V, p.b_rows);
   a.tile_n = p.tile_n;
   a.stages = p.stages;
   a.stat = reinterpret_cast<float*>(ws + p.stat);
   a.cand = reinterpret_cast<unsigned long long*>(ws + p.cand);
-  if (p.n_mblk > 1) {
+  if (p.pair) {
     a.floor = reinterpret_cast<uint32_t*>(ws + p.floor);
     if (cudaMemsetAsync(a.floor, 0, (size_t)R * 4, s) != cudaSuccess) return cuda_fail();
   }
@@ -1673,16 +1706,33 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
   f.top_logprobs = top_logprobs;
   auto launch = [&](auto nc) {
     constexpr int NC = decltype(nc)::value;
+    const int smem = lp_smem_bytes(p.b_rows, p.stages);
     cudaError_t e;
     {
       ProfScope ps(VG_KERNEL_LM_HEAD, s);
-      e = launch_dep(logprob_tiles<NC>, min(dev->sms, p.n_mblk * p.n_groups), 192, lp_smem_bytes(p.tile_n, p.stages), s,
-                     Launch::kPlain, mH, mLM, a);
+      if (p.pair) {
+        const int pairs = min(dev->lp_pairs, cdiv(p.n_mblk, 2) * p.n_groups);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * pairs);
+        cfg.blockDim = dim3(192);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = 2;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, logprob_tiles<NC, true>, mH, mLM, a);
+      } else {
+        e = launch_dep(logprob_tiles<NC, false>, min(dev->sms, p.n_groups), 192, smem, s, Launch::kPlain, mH, mLM, a);
+      }
     }
     return e == cudaSuccess ? launch_dep(logprob_finish<NC>, R, kLpFinishThreads, 0, s, Launch::kPlain, f) : e;
   };
-  const cudaError_t e = p.n_cand == 12 ? launch(std::integral_constant<int, 12>{})
-                                       : launch(std::integral_constant<int, 24>{});
+  const cudaError_t e = p.n_cand == 12 ? launch(std::integral_constant<int, 12>{}) : launch(std::integral_constant<int, 24>{});
   if (e != cudaSuccess) return cuda_fail();
   return VG_OK;
 }
