@@ -84,7 +84,7 @@ __device__ __forceinline__ float lp_unkey(uint32_t u) {
 // epilogues its own rows. All loads of a stage complete on the even CTA's barrier,
 // which expects both CTAs' bytes; the even CTA issues the MMAs. (The odd CTA
 // watching its own stages and passing them on took 1,920 us for 4,096 rows, against
-// @@ us: a round trip more than six stages cover.) Shared memory then
+// 1,080 us: a round trip more than six stages cover.) Shared memory then
 // carries 64 + 64 instead of 96 + 96 bytes a cycle at full tensor rate, operands read
 // and tiles written, against the 128 it has.
 template <int NC, bool PAIR>
@@ -409,7 +409,6 @@ struct LpFinishArgs {
   float* top_logprobs;    // [R, n_top]
 };
 
-constexpr int kLpFinishThreads = 512;
 constexpr int kLpMaxGroups = 512;
 constexpr int kLpFix = 12;  // candidates whose exact logits enter the sums: the same however many alternatives are asked for
 
@@ -422,15 +421,17 @@ constexpr int kLpFix = 12;  // candidates whose exact logits enter the sums: the
 // mass, correcting those removes most of the error. The kernel is a chain of round
 // trips (statistics and heads; the lists; the candidates' rows), each with all its
 // loads under way at once.
-template <int NC>
-__global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinishArgs a) {
-  constexpr int NW = kLpFinishThreads / 32;
+// NT threads: 512 where every row has an SM to itself and the chain's length is what
+// counts, 128 where there are many rows, so that more of them are under way (4,096
+// rows: 121 us with 512, 56 with 128).
+template <int NC, int NT>
+__global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
+  constexpr int NW = NT / 32, kOwn = kLpMaxGroups / NT;  // units a thread may own: tid, tid + NT, ..
   __shared__ float red_m[NW];
   __shared__ double red_s[NW], red_t[NW], z_s[NC + 1], s_fix[kLpFix], t_fix[kLpFix];
   __shared__ unsigned long long head[kLpMaxGroups], pool[NC * NC], best[NC];
   __shared__ unsigned long long floor_s;
   __shared__ int id_s[NC + 1], n_pool;
-  static_assert(kLpMaxGroups <= kLpFinishThreads, "one unit a thread");
   griddep_launch_dependents();
   griddep_wait();
   const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -438,30 +439,40 @@ __global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinis
   if (tid == 0) n_pool = 0, floor_s = 1ull;  // 0 keys are no candidates
   if (tid < NC) best[tid] = 0ull;
   // ---- the units' sums, rescaled to the common maximum
-  const bool mine = tid < a.n_groups;
-  float mg = -INFINITY, Sg = 0.0f, Tg = 0.0f;
-  unsigned long long first = 0ull;
-  if (mine) {
-    const float* st = a.stat + (size_t)tid * 3 * a.R + r;
-    mg = st[0], Sg = st[a.R], Tg = st[2 * (size_t)a.R];
-    first = a.cand[((size_t)tid * a.R + r) * NC];
-    head[tid] = first;
+  float mg[kOwn], Sg[kOwn], Tg[kOwn], m = -INFINITY;
+  unsigned long long first[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int g = tid + i * NT;
+    mg[i] = -INFINITY, Sg[i] = Tg[i] = 0.0f, first[i] = 0ull;
+    if (g < a.n_groups) {
+      const float* st = a.stat + (size_t)g * 3 * a.R + r;
+      mg[i] = st[0], Sg[i] = st[a.R], Tg[i] = st[2 * (size_t)a.R];
+      first[i] = a.cand[((size_t)g * a.R + r) * NC];
+      head[g] = first[i];
+    }
+    m = fmaxf(m, mg[i]);
   }
-  float m = mg;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red_m[warp] = m;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < NW; ++w) m = fmaxf(m, red_m[w]);
+  double S = 0.0, T = 0.0;
   if (warp * 32 < a.n_groups) {  // whole warps
-    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      if (i * NT >= a.n_groups) break;
+      int rank = 0;
 #pragma unroll 8
-    for (int k = 0; k < a.n_groups; ++k) rank += head[k] > first;
-    if (rank == NC - 1 && first) floor_s = first;
-    // a unit's largest term is 1 before rescaling, so the factor needs fp32 accuracy only
-    const float d = mg > -INFINITY ? mg - m : 0.0f, f = mg > -INFINITY ? ex2(d * 1.4426950408889634f) : 1.0f;
-    double S = (double)f * Sg, T = mine ? (double)f * ((double)Tg + (double)Sg * fmaxf(d, -1000.0f)) : 0.0;
+      for (int k = 0; k < a.n_groups; ++k) rank += head[k] > first[i];
+      if (rank == NC - 1 && first[i]) floor_s = first[i];
+      // a unit's largest term is 1 before rescaling, so the factor needs fp32 accuracy only
+      const float d = mg[i] > -INFINITY ? mg[i] - m : 0.0f, f = mg[i] > -INFINITY ? ex2(d * 1.4426950408889634f) : 1.0f;
+      S += (double)f * Sg[i];
+      T += (double)f * ((double)Tg[i] + (double)Sg[i] * fmaxf(d, -1000.0f));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       S += __shfl_xor_sync(0xffffffffu, S, o);
@@ -470,20 +481,22 @@ __global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinis
     if (lane == 0) red_s[warp] = S, red_t[warp] = T;
   }
   __syncthreads();
-  if (mine && first >= floor_s) {
-    const uint4* l = reinterpret_cast<const uint4*>(a.cand + ((size_t)tid * a.R + r) * NC);
-    uint4 x[NC / 2];
 #pragma unroll
-    for (int k = 0; k < NC / 2; ++k) x[k] = l[k];
+  for (int i = 0; i < kOwn; ++i)
+    if (first[i] >= floor_s) {
+      const uint4* l = reinterpret_cast<const uint4*>(a.cand + ((size_t)(tid + i * NT) * a.R + r) * NC);
+      uint4 x[NC / 2];
 #pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      const unsigned long long key = k & 1 ? (unsigned long long)x[k / 2].w << 32 | x[k / 2].z
-                                           : (unsigned long long)x[k / 2].y << 32 | x[k / 2].x;
-      if (key >= floor_s) pool[atomicAdd(&n_pool, 1)] = key;
+      for (int k = 0; k < NC / 2; ++k) x[k] = l[k];
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        const unsigned long long key = k & 1 ? (unsigned long long)x[k / 2].w << 32 | x[k / 2].z
+                                             : (unsigned long long)x[k / 2].y << 32 | x[k / 2].x;
+        if (key >= floor_s) pool[atomicAdd(&n_pool, 1)] = key;
+      }
     }
-  }
   __syncthreads();
-  for (int i = tid; i < n_pool; i += kLpFinishThreads) {
+  for (int i = tid; i < n_pool; i += NT) {
     const unsigned long long key = pool[i];
     int rank = 0;
 #pragma unroll 8
@@ -491,32 +504,50 @@ __global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinis
     if (rank < NC) best[rank] = key;
   }
   __syncthreads();
-  // ---- their logits from exact products (a product of two bf16 is exact in fp32), summed in fp64
-  for (int k = warp; k <= NC; k += NW) {
-    const int v = k < NC ? (best[k] ? (int)(0xFFFFFFFFu - (uint32_t)(best[k] & 0xFFFFFFFFull)) : -1)
-                         : (tok >= 0 && tok < a.V ? tok : -1);
-    double z = -INFINITY;
-    if (v >= 0) {
+  // ---- their logits from exact products (a product of two bf16 is exact in fp32),
+  // summed in fp64; a warp takes two candidates at a time
+  for (int k0 = warp; k0 <= NC; k0 += 2 * NW) {
+    int v[2];
+    double z[2] = {0.0, 0.0};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int k = k0 + c * NW;
+      const unsigned long long key = k < NC ? best[k] : 0ull;
+      v[c] = key ? (int)(0xFFFFFFFFu - (uint32_t)(key & 0xFFFFFFFFull)) : -1;
+      if (k == NC && tok >= 0 && tok < a.V) v[c] = tok;
+    }
+    if (v[0] >= 0 || v[1] >= 0) {
       const uint4* x = reinterpret_cast<const uint4*>(a.h + (size_t)r * a.H);
-      const uint4* w = reinterpret_cast<const uint4*>(a.lm + (size_t)v * a.H);
-      double z0 = 0.0, z1 = 0.0, z2 = 0.0, z3 = 0.0;
+      const uint4* w0 = reinterpret_cast<const uint4*>(a.lm + (size_t)(v[0] >= 0 ? v[0] : v[1]) * a.H);
+      const uint4* w1 = reinterpret_cast<const uint4*>(a.lm + (size_t)(v[1] >= 0 ? v[1] : v[0]) * a.H);
+      double y[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
 #pragma unroll 5
       for (int i = lane; i < a.H / 8; i += 32) {
-        const uint4 xv = x[i], wv = w[i];
-        z0 += (double)(bf16_lo(xv.x) * bf16_lo(wv.x));
-        z1 += (double)(bf16_hi(xv.x) * bf16_hi(wv.x));
-        z2 += (double)(bf16_lo(xv.y) * bf16_lo(wv.y));
-        z3 += (double)(bf16_hi(xv.y) * bf16_hi(wv.y));
-        z0 += (double)(bf16_lo(xv.z) * bf16_lo(wv.z));
-        z1 += (double)(bf16_hi(xv.z) * bf16_hi(wv.z));
-        z2 += (double)(bf16_lo(xv.w) * bf16_lo(wv.w));
-        z3 += (double)(bf16_hi(xv.w) * bf16_hi(wv.w));
-      }
-      z = (z0 + z1) + (z2 + z3);
+        const uint4 xv = x[i], wv[2] = {w0[i], w1[i]};
+        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t ws[4] = {wv[c].x, wv[c].y, wv[c].z, wv[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[c][0] += (double)(bf16_lo(xs[e]) * bf16_lo(ws[e]));
+            y[c][1] += (double)(bf16_hi(xs[e]) * bf16_hi(ws[e]));
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) z[c] = y[c][0] + y[c][1];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        z[0] += __shfl_xor_sync(0xffffffffu, z[0], o);
+        z[1] += __shfl_xor_sync(0xffffffffu, z[1], o);
+      }
     }
-    if (lane == 0) z_s[k] = z, id_s[k] = v;
+    if (lane < 2 && k0 + lane * NW <= NC) {
+      const int id = lane ? v[1] : v[0];
+      z_s[k0 + lane * NW] = id >= 0 ? (lane ? z[1] : z[0]) : -INFINITY;
+      id_s[k0 + lane * NW] = id;
+    }
   }
   if (tid == 0 && tok >= a.V) record_error(kErrBounds, 355);
   __syncthreads();
@@ -533,8 +564,8 @@ __global__ void __launch_bounds__(kLpFinishThreads) logprob_finish(const LpFinis
   }
   __syncthreads();
   if (warp != 0) return;
-  double S = 0.0, T = 0.0;
-  for (int w = 0; w * 32 < a.n_groups; ++w) S += red_s[w], T += red_t[w];
+  S = 0.0, T = 0.0;
+  for (int w = 0; w < NW && w * 32 < a.n_groups; ++w) S += red_s[w], T += red_t[w];
 #pragma unroll
   for (int k = 0; k < kLpFix; ++k) S += s_fix[k], T += t_fix[k];
   const double log_s = log(S), lse = (double)m + log_s;

@@ -1604,15 +1604,17 @@ LpPlan lp_plan(int R, int V, int n_top) {
   // cores bound, pairs of CTAs on 256 rows
   p.pair = p.n_mblk > 1;
   const int workers = p.pair ? kSms / 2 : kSms, n_rb = p.pair ? cdiv(p.n_mblk, 2) : 1;
-  // The busiest worker's columns, with 16 more a tile for filling the pipeline and
+  // The busiest worker's columns, with 12 more a tile for filling the pipeline and
   // 32 a unit for its lists, decide between the cuts. Pairs keep the largest tile.
+  // (129,280 rows of the LM head, 4 hidden rows: 62.4 us with five tiles of 176 an
+  // SM, 63.5 with four of 224.)
   int64_t best = -1;
   for (int tile = 256; tile >= (p.pair ? 256 : 64); tile -= 16) {
     const int n_vblk = cdiv(V, tile);
     const int most = p.pair ? 16 : cdiv(n_vblk, kSms);
     for (int g = p.pair ? 1 : most; g <= most; ++g) {
       const int64_t units = (int64_t)cdiv(n_vblk, g) * n_rb;
-      const int64_t cost = (units + workers - 1) / workers * ((int64_t)min(g, n_vblk) * (tile + 16) + 32);
+      const int64_t cost = (units + workers - 1) / workers * ((int64_t)min(g, n_vblk) * (tile + 12) + 32);
       if (cdiv(n_vblk, g) <= kLpMaxGroups && (best < 0 || cost < best)) {
         best = cost;
         p.tile_n = tile;
@@ -1730,7 +1732,9 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
         e = launch_dep(logprob_tiles<NC, false>, min(dev->sms, p.n_groups), 192, smem, s, Launch::kPlain, mH, mLM, a);
       }
     }
-    return e == cudaSuccess ? launch_dep(logprob_finish<NC>, R, kLpFinishThreads, 0, s, Launch::kPlain, f) : e;
+    if (e != cudaSuccess) return e;
+    return R <= 2 * dev->sms ? launch_dep(logprob_finish<NC, 512>, R, 512, 0, s, Launch::kPlain, f)
+                             : launch_dep(logprob_finish<NC, 128>, R, 128, 0, s, Launch::kPlain, f);
   };
   const cudaError_t e = p.n_cand == 12 ? launch(std::integral_constant<int, 12>{}) : launch(std::integral_constant<int, 24>{});
   if (e != cudaSuccess) return cuda_fail();
