@@ -90,12 +90,23 @@ __device__ __forceinline__ bool kv8_span(const Kv8AttnArgs& a, int b, Kv8Span* s
   return true;
 }
 
+// The query rows of a unit as Q^T fragments, with what belongs to each row: in a
+// CTA's shared memory where a unit has several tiles of 8 rows (32 registers a
+// lane less: 12 warps an SM without spills), else in every warp's registers.
+template <int DIM, int NT>
+struct Kv8Rows {
+  uint2 frag[NT][DIM / 16][32];  // of lane (g, t): row g, the k-step's two pairs
+  float mult[8 * NT], bias[8 * NT];
+  int last[8 * NT];
+};
+
 // One warp's running softmax over groups of 16 positions, for NT tiles of 8
 // query rows. Lane (g, t) = (lane / 4, lane % 4) holds columns (rows) 2t, 2t+1
 // of every tile.
 template <int FMT, int DIM, int NT>
 struct Kv8Warp {
-  uint32_t q[NT][DIM / 16][2];   // Q^T fragments
+  static constexpr bool kShared = NT > 1;  // the fragments are in shared memory: q holds one tile while it is set up
+  uint32_t q[kShared ? 1 : NT][DIM / 16][2];  // Q^T fragments
   float mult[NT][2];             // softmax scale * log2(e) / Q * 2^e of rows 2t, 2t+1
   int last[NT][2];               // last position those rows see (-1: none)
   float bias[NT][2];             // int8: what the 128 in every code adds to a score's sum
@@ -103,64 +114,95 @@ struct Kv8Warp {
   float o[NT][DIM / 32][2][4];   // O^T: dimensions 4 (g + 8 j) + 0..3
   float top_v;                   // largest magnitude of a value block seen: o is in units of it / Q / kKaLift
 
-  // The tile's query rows, 16 dimensions of every 64 a lane; zeros behind the real ones.
-  __device__ __forceinline__ void load(const Kv8AttnArgs& a, int b, int kvh, int tile, int n_q, int lane) {
+  // One tile of 8 query rows, 16 dimensions of every 64 a lane; zeros behind the real ones.
+  __device__ __forceinline__ void load(const Kv8AttnArgs& a, int b, int kvh, int tile8, int n_q, int lane) {
     const int g = lane >> 2, t = lane & 3, group = a.n_heads / a.c.n_kv;
+    // column g of the tile: query row r = i * group + head in the group
+    const int r = tile8 * 8 + g;
+    const bool real = r < n_q;
+    const int i = real ? r / group : 0, h = kvh * group + (real ? r - i * group : 0);
+    const __nv_bfloat16* src = a.q + ((int64_t)b * a.rows + i) * a.q_stride + h * DIM + 16 * t;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      // column g of the tile: query row r = i * group + head in the group
-      const int r = (tile * NT + nt) * 8 + g;
-      const bool real = r < n_q;
-      const int i = real ? r / group : 0, h = kvh * group + (real ? r - i * group : 0);
-      const __nv_bfloat16* src = a.q + ((int64_t)b * a.rows + i) * a.q_stride + h * DIM + 16 * t;
-#pragma unroll
-      for (int k = 0; k < DIM / 64; ++k) {
-        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-        if (real) {
-          w0 = *reinterpret_cast<const uint4*>(src + 64 * k);
-          w1 = *reinterpret_cast<const uint4*>(src + 64 * k + 8);
-        }
-        q[nt][4 * k][0] = w0.x, q[nt][4 * k][1] = w0.y, q[nt][4 * k + 1][0] = w0.z, q[nt][4 * k + 1][1] = w0.w;
-        q[nt][4 * k + 2][0] = w1.x, q[nt][4 * k + 2][1] = w1.y, q[nt][4 * k + 3][0] = w1.z, q[nt][4 * k + 3][1] = w1.w;
+    for (int k = 0; k < DIM / 64; ++k) {
+      uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+      if (real) {
+        w0 = *reinterpret_cast<const uint4*>(src + 64 * k);
+        w1 = *reinterpret_cast<const uint4*>(src + 64 * k + 8);
       }
+      q[0][4 * k][0] = w0.x, q[0][4 * k][1] = w0.y, q[0][4 * k + 1][0] = w0.z, q[0][4 * k + 1][1] = w0.w;
+      q[0][4 * k + 2][0] = w1.x, q[0][4 * k + 2][1] = w1.y, q[0][4 * k + 3][0] = w1.z, q[0][4 * k + 3][1] = w1.w;
     }
   }
 
-  // Turns the loaded rows into f16 fragments and clears the sums.
-  __device__ __forceinline__ void begin(const Kv8AttnArgs& a, int tile, const Kv8Span& s, int lane) {
-    const int g = lane >> 2, t = lane & 3, group = a.n_heads / a.c.n_kv, n_q = s.n * group;
+  // Turns the loaded rows into f16 fragments; row g's factor, bias and last position.
+  __device__ __forceinline__ void convert(const Kv8AttnArgs& a, int tile8, const Kv8Span& s, int lane, float* row_mult,
+                                          float* row_bias, int* row_last) {
+    const int group = a.n_heads / a.c.n_kv;
+    float big = 0.0f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float big = 0.0f;
+    for (int k = 0; k < DIM / 16; ++k)
 #pragma unroll
-      for (int k = 0; k < DIM / 16; ++k)
+      for (int e = 0; e < 2; ++e) big = fmaxf(big, fmaxf(fabsf(bf16_lo(q[0][k][e])), fabsf(bf16_hi(q[0][k][e]))));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    // 2^(14 - floor(log2 big)), as two factors: the product may leave the normal range
+    const int ex = big > 0.0f && big < INFINITY ? ilogbf(big) : 0, lift = 14 - ex;
+    const float up0 = __int_as_float((lift / 2 + 127) << 23), up1 = __int_as_float((lift - lift / 2 + 127) << 23);
+    float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) big = fmaxf(big, fmaxf(fabsf(bf16_lo(q[nt][k][e])), fabsf(bf16_hi(q[nt][k][e]))));
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      // 2^(14 - floor(log2 big)), as two factors: the product may leave the normal range
-      const int ex = big > 0.0f && big < INFINITY ? ilogbf(big) : 0, lift = 14 - ex;
-      const float up0 = __int_as_float((lift / 2 + 127) << 23), up1 = __int_as_float((lift - lift / 2 + 127) << 23);
-      float sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < DIM / 16; ++k)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const __half2 h2 = __floats2half2_rn(bf16_lo(q[nt][k][e]) * up0 * up1, bf16_hi(q[nt][k][e]) * up0 * up1);
-          q[nt][k][e] = *reinterpret_cast<const uint32_t*>(&h2);
-          sum += __low2float(h2) + __high2float(h2);
-        }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      sum *= kKaTiny * 128.0f;
-      const float down0 = __int_as_float((127 - lift / 2) << 23), down1 = __int_as_float((127 - (lift - lift / 2)) << 23);
-      const float back = a.scale_log2 * down0 * down1 * (FMT == kKv8Int8 ? 1.0f / kKaTiny : 1.0f);
-      const int r = (tile * NT + nt) * 8 + g, seen = r < n_q ? s.L + r / group : -1;
+    for (int k = 0; k < DIM / 16; ++k)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mult[nt][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
-        last[nt][e] = __shfl_sync(0xffffffffu, seen, 4 * (2 * t + e));
-        bias[nt][e] = FMT == kKv8Int8 ? __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e)) : 0.0f;
+        const __half2 h2 = __floats2half2_rn(bf16_lo(q[0][k][e]) * up0 * up1, bf16_hi(q[0][k][e]) * up0 * up1);
+        q[0][k][e] = *reinterpret_cast<const uint32_t*>(&h2);
+        sum += __low2float(h2) + __high2float(h2);
+      }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    const float down0 = __int_as_float((127 - lift / 2) << 23), down1 = __int_as_float((127 - (lift - lift / 2)) << 23);
+    const int r = tile8 * 8 + (lane >> 2);
+    *row_bias = FMT == kKv8Int8 ? sum * (kKaTiny * 128.0f) : 0.0f;
+    *row_mult = a.scale_log2 * down0 * down1 * (FMT == kKv8Int8 ? 1.0f / kKaTiny : 1.0f);
+    *row_last = r < s.n * group ? s.L + r / group : -1;
+  }
+
+  // Sets up the loaded rows and clears the sums. With shared fragments warp nt has
+  // loaded tile nt, and the CTA meets here.
+  __device__ __forceinline__ void begin(const Kv8AttnArgs& a, int tile, const Kv8Span& s, int warp, int lane,
+                                        Kv8Rows<DIM, NT>* rows) {
+    const int t = lane & 3;
+    float row_mult, row_bias;
+    int row_last;
+    if constexpr (kShared) {
+      if (warp < NT) {
+        convert(a, tile * NT + warp, s, lane, &row_mult, &row_bias, &row_last);
+#pragma unroll
+        for (int k = 0; k < DIM / 16; ++k) rows->frag[warp][k][lane] = make_uint2(q[0][k][0], q[0][k][1]);
+        if (t == 0) {
+          const int r = warp * 8 + (lane >> 2);
+          rows->mult[r] = row_mult;
+          rows->bias[r] = row_bias;
+          rows->last[r] = row_last;
+        }
+      }
+      __syncthreads();
+    } else {
+      convert(a, tile, s, lane, &row_mult, &row_bias, &row_last);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 2 * t + e;
+        if constexpr (kShared) {
+          mult[nt][e] = rows->mult[nt * 8 + r];
+          bias[nt][e] = rows->bias[nt * 8 + r];
+          last[nt][e] = rows->last[nt * 8 + r];
+        } else {
+          mult[nt][e] = __shfl_sync(0xffffffffu, row_mult, 4 * r);
+          bias[nt][e] = __shfl_sync(0xffffffffu, row_bias, 4 * r);
+          last[nt][e] = __shfl_sync(0xffffffffu, row_last, 4 * r);
+        }
         m[nt][e] = -INFINITY;
         l[nt][e] = 0.0f;
       }
@@ -177,7 +219,8 @@ struct Kv8Warp {
   // subtraction; 128 times the row's sum is taken off the score. (Values do not:
   // their weights are all positive, so the 128s would not cancel and the sums
   // would lose what they add.)
-  __device__ __forceinline__ void scores(const uint4 (&kf)[DIM / 32], float (&s)[NT][4]) const {
+  __device__ __forceinline__ void scores(const uint4 (&kf)[DIM / 32], float (&s)[NT][4], const Kv8Rows<DIM, NT>* rows,
+                                         int lane) const {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -197,7 +240,14 @@ struct Kv8Warp {
           kv8_to_half<FMT>(xc[w], &a1, &a3);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, q[nt][h * 4 + w][0], q[nt][h * 4 + w][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (kShared) {
+            const uint2 f = rows->frag[nt][h * 4 + w][lane];
+            mma_f16(s[nt], a0, a1, a2, a3, f.x, f.y);
+          } else {
+            mma_f16(s[nt], a0, a1, a2, a3, q[nt][h * 4 + w][0], q[nt][h * 4 + w][1]);
+          }
+        }
       }
     }
   }
@@ -330,6 +380,7 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
   constexpr int W = ka_warps(NT), kThreads = 32 * W, kTile = kKv8Group * W, kRowW = DIM + 4;
   __shared__ __align__(16) float wo[W * 8 * NT * kRowW];
   __shared__ float wm[W * 8 * NT], wl[W * 8 * NT];
+  __shared__ Kv8Rows<DIM, NT> rows_s;  // (unused with one tile of rows)
   __shared__ int start[kKaTable + 1];  // first tile of each sequence
   __shared__ int4 span[kKaTable];          // lo, hi, L, n
   __shared__ int sums[kKaTable / 32];
@@ -425,7 +476,7 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
   auto enter = [&]() {  // a unit's share: request its query rows, then its first tile
     const int4 sp = span[p.b];
     s = Kv8Span{sp.z, sp.x, sp.y, sp.w};
-    w.load(a, a.b0 + p.b, p.kvh, p.tile, s.n * group, lane);
+    if (NT == 1 || warp < NT) w.load(a, a.b0 + p.b, p.kvh, p.tile * NT + (NT == 1 ? 0 : warp), s.n * group, lane);
     p0 = s.lo / kKv8Group * kKv8Group + p.j * kTile + warp * kKv8Group;
     const size_t head = (size_t)(a.b0 + p.b) * a.c.n_kv + p.kvh;
     kp = a.c.k + (head * a.c.L_max + p0) * DIM + k_at;
@@ -442,12 +493,12 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
   for (int T = t0; T < t1;) {
     const int seg0 = T - p.j, seg1 = seg0 + p.n;  // the unit's tiles
     const int n = min(seg1, t1) - T;              // those of this CTA
-    w.begin(a, p.tile, s, lane);
+    w.begin(a, p.tile, s, warp, lane, &rows_s);
     for (int i = 0; i < n && p0 < s.hi; ++i) {
       const bool more = i + 1 < n && p0 + kTile < s.hi;
       float z[NT][4];
       uint32_t b0[NT], b1[NT];
-      w.scores(kf, z);
+      w.scores(kf, z, &rows_s, lane);
       const float ks_now = ks, vs_now = vs;
       if (more) {
         kp += kTile * DIM;
