@@ -149,10 +149,25 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
-    if stream is None:
+_torch = None
+
+
+def _t():
+    """torch, imported on first use."""
+    global _torch
+    if _torch is None:
         import torch
 
+        _torch = torch
+    return _torch
+
+
+def _stream(stream):
+    if stream is None:
+        torch = _t()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:  # the same handle, without the 3 us that a Stream object takes
+            return ctypes.c_void_p(raw(torch.cuda.current_device()))
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
@@ -356,44 +371,50 @@ def vg_attn_verify(B, K, x, w_qkv, w_o, kv_cache, lens, out, workspace, o_out=No
 
 
 # ------------------------------------------------------------ 8-bit KV cache
+# A call of these costs a few microseconds on the GPU at its smallest, so the
+# checks below are kept to a comparison each.
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
-def _on(device, **tensors):
-    """Every tensor given lies on that device, and it is the current one (the
-    library launches on the current device)."""
-    import torch
-
-    if device.type == "cuda":
-        _need(device.index == torch.cuda.current_device(), f"tensors are on {device}, which is not the current device")
-    for name, t in tensors.items():
+def _same_device(device, *tensors):
+    """Every tensor lies on `device`, and if that is a CUDA device it is the
+    current one: the library launches on the current device."""
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+            raise ValueError(f"a tensor is on {t.device}, not on {device}")
+    index = device.index
+    if index is not None and index != _t().cuda.current_device():
+        raise ValueError(f"tensors are on {device}, which is not the current device")
 
 
 def _rows(name, t, n, width, dtypes):
     """Row stride of a [n, width] matrix with dense rows."""
     if t is None:
         return 0
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or t.dtype not in dtypes:
+    if t.shape != (n, width) or t.dtype not in dtypes:
         raise ValueError(f"{name} must be [{n}, {width}] of {dtypes}, got {tuple(t.shape)} of {t.dtype}")
-    if width > 1 and t.stride(1) != 1:
+    step, one = t.stride()
+    if one != 1 and width > 1:
         raise ValueError(f"{name} must have dense rows")
-    return t.stride(0) if n > 1 else max(t.stride(0), width)
+    return step if n > 1 else max(step, width)
 
 
 def _dense(name, t, shape, dtype):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()):
+    if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()):
         raise ValueError(f"{name} must be dense {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _bytes_of(workspace):
     if workspace is None:
         return 0
     _need(workspace.is_contiguous(), "workspace must be contiguous")
-    return workspace.numel() * workspace.element_size()
+    return workspace.nbytes
 
 
 def make_kv8(k, v, k_amax, v_amax):
@@ -401,8 +422,7 @@ def make_kv8(k, v, k_amax, v_amax):
     codes (torch.int8 or torch.float8_e4m3fn; inside a (sequence, head) they lie
     in the order include/vgv.h documents), k_amax and v_amax fp32
     [B, n_kv, L_max / block]. The handle keeps the tensors alive."""
-    import torch
-
+    torch = _t()
     formats = {torch.int8: VG_KV8_INT8, torch.float8_e4m3fn: VG_KV8_E4M3}
     _need(k.dim() == 4 and k.dtype in formats, "k must be [B, n_kv, L_max, dim] of int8 or float8_e4m3fn")
     B, n_kv, L_max, dim = k.shape
@@ -418,78 +438,74 @@ def make_kv8(k, v, k_amax, v_amax):
                k_amax.data_ptr(), v_amax.data_ptr())
     c.tensors = (k, v, k_amax, v_amax)
     c.device = k.device
+    c.ref = ctypes.byref(c)
     return c
 
 
 def vg_kv8_append(cache, rows, k, v, pos, n_new=None, stream=None):
     """Quantises `rows` new rows per sequence (k, v: bf16 [B * rows, n_kv * dim],
     any row stride) into the cache at positions pos[b] .. (the first n_new[b])."""
-    import torch
-
+    torch = _t()
     B, width, bf16 = cache.B, cache.n_kv * cache.dim, (torch.bfloat16,)
     ks, vs = _rows("k", k, B * rows, width, bf16), _rows("v", v, B * rows, width, bf16)
     _dense("pos", pos, (B,), torch.int32)
     _dense("n_new", n_new, (B,), torch.int32)
-    _on(cache.device, k=k, v=v, pos=pos, n_new=n_new)
-    _check(load().vg_kv8_append(ctypes.byref(cache), rows, _ptr(k), ks, _ptr(v), vs, _ptr(pos), _ptr(n_new),
-                                _stream(stream)), "vg_kv8_append")
+    _same_device(cache.device, k, v, pos, n_new)
+    _check(load().vg_kv8_append(cache.ref, rows, _at(k), ks, _at(v), vs, _at(pos), _at(n_new), _stream(stream)),
+           "vg_kv8_append")
 
 
 def vg_kv8_read(cache, rows, pos, k_out, v_out, n_rows=None, stream=None):
     """Positions pos[b] .. pos[b] + n_rows[b] - 1 of every sequence as values, into
     rows b * rows .. of k_out and v_out ([B * rows, n_kv * dim], bf16 or fp32
     alike; either may be None)."""
-    import torch
-
+    torch = _t()
     B, width, types = cache.B, cache.n_kv * cache.dim, (torch.bfloat16, torch.float32)
     ks, vs = _rows("k_out", k_out, B * rows, width, types), _rows("v_out", v_out, B * rows, width, types)
-    _need(k_out is None or v_out is None or k_out.dtype == v_out.dtype, "k_out and v_out must have one type")
+    out = k_out if k_out is not None else v_out
+    _need(v_out is None or out.dtype is v_out.dtype, "k_out and v_out must have one type")
     _dense("pos", pos, (B,), torch.int32)
     _dense("n_rows", n_rows, (B,), torch.int32)
-    _on(cache.device, k_out=k_out, v_out=v_out, pos=pos, n_rows=n_rows)
-    out = k_out if k_out is not None else v_out
-    kind = VG_F32 if out is not None and out.dtype == torch.float32 else VG_BF16
-    _check(load().vg_kv8_read(ctypes.byref(cache), rows, _ptr(pos), _ptr(n_rows), kind, _ptr(k_out), ks, _ptr(v_out), vs,
+    _same_device(cache.device, k_out, v_out, pos, n_rows)
+    kind = VG_F32 if out is not None and out.dtype is torch.float32 else VG_BF16
+    _check(load().vg_kv8_read(cache.ref, rows, _at(pos), _at(n_rows), kind, _at(k_out), ks, _at(v_out), vs,
                               _stream(stream)), "vg_kv8_read")
 
 
 def vg_kv8_attn_workspace_bytes(cache, rows, n_heads):
-    return load().vg_kv8_attn_workspace_bytes(ctypes.byref(cache), rows, n_heads)
+    return load().vg_kv8_attn_workspace_bytes(cache.ref, rows, n_heads)
 
 
 def vg_kv8_attn(cache, rows, n_heads, q, lens, scale, o, workspace, first=None, n_new=None, stream=None):
     """Attention of `rows` query rows per sequence (q, o: bf16 [B * rows,
     n_heads * dim], any row stride) over the cache."""
-    import torch
-
+    torch = _t()
     B, width, bf16 = cache.B, n_heads * cache.dim, (torch.bfloat16,)
     qs, os_ = _rows("q", q, B * rows, width, bf16), _rows("o", o, B * rows, width, bf16)
     _dense("lens", lens, (B,), torch.int32)
     _dense("first", first, (B,), torch.int32)
     _dense("n_new", n_new, (B,), torch.int32)
-    _on(cache.device, q=q, o=o, lens=lens, first=first, n_new=n_new, workspace=workspace)
-    _check(load().vg_kv8_attn(ctypes.byref(cache), rows, n_heads, _ptr(q), qs, _ptr(lens), _ptr(first), _ptr(n_new), scale,
-                              _ptr(o), os_, _ptr(workspace), _bytes_of(workspace), _stream(stream)), "vg_kv8_attn")
+    _same_device(cache.device, q, o, lens, first, n_new, workspace)
+    _check(load().vg_kv8_attn(cache.ref, rows, n_heads, _at(q), qs, _at(lens), _at(first), _at(n_new), scale, _at(o), os_,
+                              _at(workspace), _bytes_of(workspace), _stream(stream)), "vg_kv8_attn")
 
 
 def vg_attn_verify_kv8_workspace_bytes(cache, K):
-    return load().vg_attn_verify_kv8_workspace_bytes(ctypes.byref(cache), K)
+    return load().vg_attn_verify_kv8_workspace_bytes(cache.ref, K)
 
 
 def vg_attn_verify_kv8(cache, K, x, w_qkv, w_o, lens, out, workspace, o_out=None, stream=None):
     """One attention layer of a verify step on an 8-bit cache (vg_attn_verify's
     arguments; the batch is the cache's)."""
-    import torch
-
+    torch = _t()
     R, H, bf16 = cache.B * (K + 1), cache.n_kv * cache.dim, torch.bfloat16
     for name, t, shape in (("x", x, (R, H)), ("w_qkv", w_qkv, (3 * H, H)), ("w_o", w_o, (H, H)), ("out", out, (R, H)),
                            ("o_out", o_out, (R, H))):
         _dense(name, t, shape, bf16)
     _dense("lens", lens, (cache.B,), torch.int32)
-    _on(cache.device, x=x, w_qkv=w_qkv, w_o=w_o, lens=lens, out=out, o_out=o_out, workspace=workspace)
-    _check(load().vg_attn_verify_kv8(ctypes.byref(cache), K, _ptr(x), _ptr(w_qkv), _ptr(w_o), _ptr(lens), _ptr(out),
-                                     _ptr(o_out), _ptr(workspace), _bytes_of(workspace), _stream(stream)),
-           "vg_attn_verify_kv8")
+    _same_device(cache.device, x, w_qkv, w_o, lens, out, o_out, workspace)
+    _check(load().vg_attn_verify_kv8(cache.ref, K, _at(x), _at(w_qkv), _at(w_o), _at(lens), _at(out), _at(o_out),
+                                     _at(workspace), _bytes_of(workspace), _stream(stream)), "vg_attn_verify_kv8")
 
 
 # ------------------------------------------------------------ log probabilities
@@ -501,8 +517,7 @@ def vg_token_logprobs(h, lm_head, tokens, logprob, entropy, top_ids, top_logprob
     """Log probabilities of tokens[r] after hidden row h[r], the entropy and the
     top_ids.shape[1] most likely tokens of each row; tokens with logprob, entropy,
     and top_ids with top_logprobs may be None."""
-    import torch
-
+    torch = _t()
     _need(h.dim() == 2 and lm_head.dim() == 2, "h must be [R, H], lm_head [V, H]")
     (R, H), V = h.shape, lm_head.shape[0]
     n_top = 0 if top_ids is None else top_ids.shape[-1]
@@ -513,8 +528,7 @@ def vg_token_logprobs(h, lm_head, tokens, logprob, entropy, top_ids, top_logprob
     _dense("entropy", entropy, (R,), torch.float32)
     _dense("top_ids", top_ids, (R, n_top), torch.int32)
     _dense("top_logprobs", top_logprobs, (R, n_top), torch.float32)
-    _on(h.device, lm_head=lm_head, tokens=tokens, logprob=logprob, entropy=entropy, top_ids=top_ids,
-        top_logprobs=top_logprobs, workspace=workspace)
-    _check(load().vg_token_logprobs(R, H, V, _ptr(h), _ptr(lm_head), _ptr(tokens), n_top, _ptr(logprob), _ptr(entropy),
-                                    _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace), _bytes_of(workspace),
+    _same_device(h.device, lm_head, tokens, logprob, entropy, top_ids, top_logprobs, workspace)
+    _check(load().vg_token_logprobs(R, H, V, _at(h), _at(lm_head), _at(tokens), n_top, _at(logprob), _at(entropy),
+                                    _at(top_ids), _at(top_logprobs), _at(workspace), _bytes_of(workspace),
                                     _stream(stream)), "vg_token_logprobs")

@@ -69,7 +69,7 @@ constexpr int kPreL2Chunks = VG_PRE_L2_CHUNKS;  // further k-chunks of the first
 struct DevState {
   bool init = false;
   int sms = 0;
-  int lp_pairs = 0;  // pairs of CTAs of the log-probability kernel that run at once
+  int lp_pairs = 0;  // see lp_pairs(); 0: not asked yet
 };
 DevState g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -158,23 +158,11 @@ vg_status device_state(DevState** out) {
           cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
               cudaSuccess)
         return cuda_fail();
-    {  // pairs of CTAs that fit the GPU at once
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(d.sms / 2 * 2);
-      cfg.blockDim = dim3(192);
-      cfg.dynamicSmemBytes = kMaxSmemBytes;
-      cudaLaunchAttribute at[1];
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = 2;
-      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-      cfg.attrs = at;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&d.lp_pairs, vg::logprob_tiles<24, true>, &cfg) != cudaSuccess || d.lp_pairs < 1)
-        return cuda_fail();
-    }
     // Kernels that follow each other with dependent launches share SMs only if
     // their shared-memory configurations agree: every kernel of the decode
-    // chain asks for the largest shared-memory carveout.
+    // chain asks for the largest shared-memory carveout. (Not the 8-bit attention,
+    // which needs its L1 for the blocks' magnitudes: 37 against 33 us at B = 32,
+    // L = 2,048.)
     {
       const int kMax = cudaSharedmemCarveoutMaxShared;
       const cudaFuncAttribute kC = cudaFuncAttributePreferredSharedMemoryCarveout;
@@ -204,6 +192,28 @@ vg_status device_state(DevState** out) {
     d.init = true;
   }
   *out = &d;
+  return VG_OK;
+}
+
+// Pairs of CTAs of the log-probability kernel that the device runs at once.
+vg_status lp_pairs(DevState* d, int* out) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (d->lp_pairs == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(d->sms / 2 * 2);
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = kMaxSmemBytes;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, vg::logprob_tiles<24, true>, &cfg) != cudaSuccess || n < 1) return cuda_fail();
+    d->lp_pairs = n;
+  }
+  *out = d->lp_pairs;
   return VG_OK;
 }
 
@@ -1706,6 +1716,11 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
   f.entropy = entropy;
   f.top_ids = top_ids;
   f.top_logprobs = top_logprobs;
+  int pairs = 0;
+  if (p.pair) {
+    if ((st = lp_pairs(dev, &pairs)) != VG_OK) return st;
+    pairs = min(pairs, cdiv(p.n_mblk, 2) * p.n_groups);
+  }
   auto launch = [&](auto nc) {
     constexpr int NC = decltype(nc)::value;
     const int smem = lp_smem_bytes(p.b_rows, p.stages);
@@ -1713,7 +1728,6 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
     {
       ProfScope ps(VG_KERNEL_LM_HEAD, s);
       if (p.pair) {
-        const int pairs = min(dev->lp_pairs, cdiv(p.n_mblk, 2) * p.n_groups);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * pairs);
         cfg.blockDim = dim3(192);
