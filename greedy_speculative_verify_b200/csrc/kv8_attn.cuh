@@ -26,6 +26,17 @@
 // merged in shared memory. A unit that lies in several CTAs' shares leaves
 // partials, which the last of them to finish merges in CTA order, so results do
 // not depend on timing.
+//
+// Bound by HBM where caches are long: 16 sequences x 10 heads at 32,760 positions,
+// 8 rows each, 205 us for 1.34 GB (6.5 TB/s, what a copy reaches). At 2,048
+// positions (32 sequences, 1,650 on average, 135 MB) 33 us against 21: about 5 us
+// until every SM has its first tile, 14 tiles of 1.2 us, 1.5 us a unit's turn, 4 us
+// for the units that CTAs share. With 16 rows to a kv head (32 heads on 8, 491 MB)
+// 109 us against 75: 12 warps an SM wait for their own chains of products. Feeding
+// the warps through shared memory instead (bulk copies by a producer warp, rings
+// of their own, or 16-byte asynchronous copies) took 264, 350 and 235 us where
+// this takes 205: the same loads plus the instructions to wait for and re-read
+// them; requesting tiles into L2 ahead of time changed nothing.
 #pragma once
 #include "attention.cuh"
 #include "kv8.cuh"
@@ -56,7 +67,8 @@ struct Kv8AttnArgs {
 };
 
 // Warps per CTA and CTAs per SM: 16 warps of at most 128 registers where a unit
-// has up to 8 query rows, 12 of at most 168 where it has 16.
+// has up to 8 query rows (as 4 x 4 instead of 8 x 2: 36.0 us where this takes
+// 33.4), 12 of at most 168 where it has 16 (8 of 240: 120 us where this takes 109).
 __host__ __device__ constexpr int ka_warps(int nt) { return nt == 1 ? 8 : 4; }
 __host__ __device__ constexpr int ka_ctas(int nt) { return nt == 1 ? 2 : 3; }
 
@@ -382,11 +394,11 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
   __shared__ float wm[W * 8 * NT], wl[W * 8 * NT];
   __shared__ Kv8Rows<DIM, NT> rows_s;  // (unused with one tile of rows)
   __shared__ int start[kKaTable + 1];  // first tile of each sequence
-  __shared__ int4 span[kKaTable];          // lo, hi, L, n
+  __shared__ int4 span[kKaTable];      // lo, hi, L, n
   __shared__ int sums[kKaTable / 32];
   __shared__ int last_s[2];
-  __shared__ int ends[2][2];   // their first and last CTA
   __shared__ KaPlace edge[2];  // the units of this share's first and last tile
+  __shared__ int ends[2][2];   // their first and last CTA
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.n_heads / a.c.n_kv, units = a.c.n_kv * a.n_tiles;  // units per sequence
   griddep_launch_dependents();
@@ -596,28 +608,26 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
     if (!last_s[side]) continue;
     const KaPlace e = edge[side];
     const int c0 = ends[side][0], c1 = ends[side][1];
-    {
-      const int n_q = span[e.b].w * group;
-      for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
-        const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
-        float mm = -INFINITY, ls = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int n_q = span[e.b].w * group;
+    for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
+      const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
+      float mm = -INFINITY, ls = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-          const float* x = a.part + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * (8 * NT) + r) * (DIM + 2);
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(x + DIM));
-          const float2 v0 = __ldcg(reinterpret_cast<const float2*>(x + d)), v1 = __ldcg(reinterpret_cast<const float2*>(x + d + 2));
-          const float now = fmaxf(mm, ml.x), base = now > -INFINITY ? now : 0.0f;
-          const float f = ex2(mm - base), h = ex2(ml.x - base);
-          mm = now;
-          ls = ls * f + ml.y * h;
-          acc.x = acc.x * f + v0.x * h, acc.y = acc.y * f + v0.y * h;
-          acc.z = acc.z * f + v1.x * h, acc.w = acc.w * f + v1.y * h;
-        }
-        ka_store<DIM, NT>(a, e, n_q, r, d, acc, ls);
+      for (int c = c0; c <= c1; ++c) {
+        const float* x = a.part + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * (8 * NT) + r) * (DIM + 2);
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(x + DIM));
+        const float2 v0 = __ldcg(reinterpret_cast<const float2*>(x + d)), v1 = __ldcg(reinterpret_cast<const float2*>(x + d + 2));
+        const float now = fmaxf(mm, ml.x), base = now > -INFINITY ? now : 0.0f;
+        const float f = ex2(mm - base), h = ex2(ml.x - base);
+        mm = now;
+        ls = ls * f + ml.y * h;
+        acc.x = acc.x * f + v0.x * h, acc.y = acc.y * f + v0.y * h;
+        acc.z = acc.z * f + v1.x * h, acc.w = acc.w * f + v1.y * h;
       }
-      if (tid == 0) atomicExch(a.arrived + c0, 0u);
+      ka_store<DIM, NT>(a, e, n_q, r, d, acc, ls);
     }
+    if (tid == 0) atomicExch(a.arrived + c0, 0u);
   }
 }
 

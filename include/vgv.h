@@ -487,8 +487,8 @@ vg_status vg_kv8_read(const vg_kv8* c, int32_t rows, const int32_t* pos, const i
  * h / (n_heads / n_kv), at most 16 to a head. Rows i >= n_new[b] (n_new NULL:
  * none) are not read and get o = 0. lens[b] < 0, first[b] < 0, n_new[b] outside
  * [0, rows] or lens[b] + n_new[b] > L_max records VG_ERR_DEVICE_BOUNDS and gives
- * o = 0 for that sequence. scale > 0; a row with scores beyond the fp32 range
- * gets NaN.
+ * o = 0 for that sequence. scale > 0; of a row with scores beyond the fp32
+ * range nothing is promised.
  * Precision: codes enter both products exactly (f16 operands, fp32 sums), query
  * rows exactly down to 2^-29 of their largest element; softmax weights are
  * rounded to 2^-11 of themselves (those that, times their block's share of the

@@ -228,6 +228,9 @@ def check_attention(c, rows, n_heads, lens, seed=0, first=None, n_new=None, pad=
     q = oracle.widen(oracle.round_bf16_bits(g.normal(0, q_size, (c.B, rows, n_heads, c.dim))))
     qd = torch.full((c.B * rows, w + pad), float("nan"), dtype=torch.bfloat16, device="cuda")
     qd[:, :w] = torch.from_numpy(q.reshape(-1, w).astype(np.float32)).to("cuda")
+    if n_new is not None:  # padded rows are not read
+        for b in range(c.B):
+            qd[b * rows + int(n_new[b]):(b + 1) * rows] = float("nan")
     gd = Guarded()
     od = gd.empty((c.B * rows, w + pad), torch.bfloat16, fill=-3.0)
     ws = gd.empty((max(16, vgv.vg_kv8_attn_workspace_bytes(c.h, rows, n_heads)),), torch.uint8, fill=0)
@@ -235,6 +238,10 @@ def check_attention(c, rows, n_heads, lens, seed=0, first=None, n_new=None, pad=
     vgv.vg_kv8_attn(c.h, rows, n_heads, qd[:, :w], i32(lens), scale, od[:, :w], ws, **args)
     ok()
     gd.check()
+    once = od.clone()
+    vgv.vg_kv8_attn(c.h, rows, n_heads, qd[:, :w], i32(lens), scale, od[:, :w], ws, **args)
+    ok()
+    assert torch.equal(once, od)  # the same bits again
     assert int(ws[:2048].count_nonzero()) == 0  # its counters are zero again
     k, v = c.values()
     ref, mag, size = kv8.attention(q, k, v, lens, scale, first, n_new)
