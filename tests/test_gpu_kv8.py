@@ -273,7 +273,7 @@ def check_attention(c, rows, n_heads, lens, seed=0, first=None, n_new=None, pad=
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dim,block,n_kv,group,rows", [
     (128, 64, 10, 1, 4), (128, 16, 1, 1, 1), (64, 16, 2, 4, 3), (128, 32, 2, 8, 8), (64, 128, 3, 2, 8), (128, 128, 1, 16, 7),
-    (128, 64, 2, 3, 5), (64, 32, 1, 8, 1)])
+    (128, 64, 2, 3, 5), (64, 32, 1, 8, 1), (128, 64, 2, 4, 8), (64, 16, 1, 3, 8), (128, 32, 1, 5, 7)])
 def test_attention(fmt, dim, block, n_kv, group, rows):
     """Ragged lengths from no cached position to several hundred, ends inside
     groups, blocks and chunks."""
