@@ -82,6 +82,12 @@ struct LpList {
   }
 };
 
+// The largest fp32 value below x (x not NaN; zero: below -0).
+__device__ __forceinline__ float lp_below(float x) {
+  const int b = __float_as_int(x);
+  return x == 0.0f ? __int_as_float(0x80000001) : x == -INFINITY ? x : __int_as_float(b > 0 ? b - 1 : b + 1);
+}
+
 // An fp32 logit's image in the order of argmax_key's high word, and back.
 __device__ __forceinline__ float lp_unkey(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
@@ -329,6 +335,35 @@ __global__ void __launch_bounds__(192, 1)
         tc_fence_after();
         const uint32_t t0 = tmem_base + ((uint32_t)(q * 32) << 16) + ab * 256;
         const int v0 = vb * a.tile_n, cols = busy ? min(a.tile_n, a.V - v0) : 0;
+        if (vb == g * a.group_tiles && __any_sync(0xffffffffu, least == -INFINITY && r < a.R)) {
+          // A bound to start with: NC groups of kLpBound columns have a maximum of
+          // at least the NC-th largest of the groups' maxima, so NC logits reach it.
+          // Finding it moves values alone (two instructions a place, and groups
+          // follow each other through the list), where a column that enters costs
+          // five a place: of a first tile of 176 columns 31 enter the list of 24
+          // then, and 72 without.
+          constexpr int kLpBound = NC == 12 ? 8 : 4;
+#pragma unroll 1
+          for (int c0 = 0; c0 + kLpChunk <= cols; c0 += kLpChunk) {
+            uint32_t zb[kLpChunk];
+            tmem_ld16(t0 + c0, zb);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < kLpChunk; j += kLpBound) {
+              float x = __uint_as_float(zb[j]);
+#pragma unroll
+              for (int i = 1; i < kLpBound; ++i) x = fmaxf(x, __uint_as_float(zb[j + i]));
+#pragma unroll
+              for (int k = 0; k < NC; ++k) {
+                const float z = list.z[k];
+                list.z[k] = fmaxf(z, x);
+                x = fminf(z, x);
+              }
+            }
+          }
+          least = fmaxf(least, lp_below(list.z[NC - 1]));
+          list.clear();
+        }
 #pragma unroll 1
         for (int c0 = 0; c0 < cols; c0 += kLpChunk) {
           uint32_t zb[kLpChunk];

@@ -146,6 +146,24 @@ def test_rising_logits():
     assert np.array_equal(ids, order)  # ties to the lower index
 
 
+@pytest.mark.parametrize("n_top", [8, 20])
+def test_alternatives_beside_each_other(n_top):
+    """All the largest logits in neighbouring columns (one group of a bound), at
+    the start of a vocabulary, over a tile's end and at its end; with ties."""
+    V, H, R = 2100, 64, 9
+    at = [0, 1, 170, 250, 255, 700, 1750, V - n_top, V - n_top - 3]
+    h, lm = np.zeros((R, H)), np.full((V, H), -1.0)
+    for r in range(R):
+        h[r, r] = 1.0
+        lm[at[r]:at[r] + n_top, r] = 8.0 + np.arange(n_top) // 2  # pairs of equal logits
+    lm[:, 10:] = 0
+    hb, lb = oracle.round_bf16_bits(h), oracle.round_bf16_bits(lm)
+    lp, _, _ = kv8.logprobs(hb, lb)
+    ids = call(dev(hb), dev(lb), None, n_top)[2]
+    order = np.lexsort((np.broadcast_to(np.arange(V), lp.shape), -np.round(lp, 9)), axis=1)[:, :n_top]
+    assert np.array_equal(ids, order)
+
+
 def test_order_of_alternatives_closer_than_fp32():
     """Two tokens whose logits differ by less than an fp32 sum resolves, in both
     index orders: the larger exact logit comes first."""
