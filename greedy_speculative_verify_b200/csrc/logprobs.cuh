@@ -474,13 +474,14 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   __shared__ double red_s[NW], red_t[NW], z_s[NC + 1], s_fix[kLpFix], t_fix[kLpFix];
   __shared__ unsigned long long head[kLpMaxGroups], pool[NC * NC], best[NC];
   __shared__ unsigned long long floor_s;
-  __shared__ int id_s[NC + 1], n_pool;
+  __shared__ int id_s[NC + 1], rank_s[NC], head_rank[kLpMaxGroups], n_pool;
   griddep_launch_dependents();
   griddep_wait();
   const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tok = a.tokens ? a.tokens[r] : -1;
   if (tid == 0) n_pool = 0, floor_s = 1ull;  // 0 keys are no candidates
-  if (tid < NC) best[tid] = 0ull;
+  if (tid < NC) best[tid] = 0ull, rank_s[tid] = 0;
+  for (int g = tid; g < a.n_groups; g += NT) head_rank[g] = 0;
   // ---- the units' sums, rescaled to the common maximum
   float mg[kOwn], Sg[kOwn], Tg[kOwn], m = -INFINITY;
   unsigned long long first[kOwn];
@@ -502,15 +503,23 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < NW; ++w) m = fmaxf(m, red_m[w]);
+  // ranks of the units' first candidates, every thread with a part of the comparisons
+  {
+    const int parts = max(1, NT / a.n_groups), per = cdiv(a.n_groups, parts);
+    for (int i = tid; i < parts * a.n_groups; i += NT) {
+      const int part = i / a.n_groups, g = i - part * a.n_groups, k1 = min(a.n_groups, (part + 1) * per);
+      const unsigned long long key = head[g];
+      int above = 0;
+#pragma unroll 8
+      for (int k = part * per; k < k1; ++k) above += head[k] > key;
+      if (above) atomicAdd(&head_rank[g], above);
+    }
+  }
   double S = 0.0, T = 0.0;
   if (warp * 32 < a.n_groups) {  // whole warps
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
       if (i * NT >= a.n_groups) break;
-      int rank = 0;
-#pragma unroll 8
-      for (int k = 0; k < a.n_groups; ++k) rank += head[k] > first[i];
-      if (rank == NC - 1 && first[i]) floor_s = first[i];
       // a unit's largest term is 1 before rescaling, so the factor needs fp32 accuracy only
       const float d = mg[i] > -INFINITY ? mg[i] - m : 0.0f, f = mg[i] > -INFINITY ? ex2(d * 1.4426950408889634f) : 1.0f;
       S += (double)f * Sg[i];
@@ -523,6 +532,11 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
     }
     if (lane == 0) red_s[warp] = S, red_t[warp] = T;
   }
+  __syncthreads();
+  // (the lists of the NC units with the largest first candidates; their smallest is the bound)
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i)
+    if (first[i] && head_rank[tid + i * NT] == NC - 1) floor_s = first[i];
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kOwn; ++i)
@@ -605,33 +619,31 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
     }
     s_fix[tid] = ds, t_fix[tid] = dt;
   }
+  // ---- order: rank of each candidate by (logit, lower index first); those that are
+  // missing (fewer logits above -inf than asked for) come last, in list order
+  for (int i = tid; i < NC * NC; i += NT) {
+    const int c = i / NC, k = i - c * NC, vc = id_s[c], vk = id_s[k];
+    const bool ahead = vk < 0 ? (vc < 0 && k < c) : (vc < 0 || z_s[k] > z_s[c] || (z_s[k] == z_s[c] && vk < vc));
+    if (ahead && k != c) atomicAdd(&rank_s[c], 1);
+  }
   __syncthreads();
   if (warp != 0) return;
-  S = 0.0, T = 0.0;
-  for (int w = 0; w < NW && w * 32 < a.n_groups; ++w) S += red_s[w], T += red_t[w];
+  S = T = 0.0;
+  if (lane < NW && lane * 32 < a.n_groups) S = red_s[lane], T = red_t[lane];
+  if (lane < kLpFix) S += s_fix[lane], T += t_fix[lane];
 #pragma unroll
-  for (int k = 0; k < kLpFix; ++k) S += s_fix[k], T += t_fix[k];
+  for (int o = 16; o > 0; o >>= 1) {
+    S += __shfl_xor_sync(0xffffffffu, S, o);
+    T += __shfl_xor_sync(0xffffffffu, T, o);
+  }
   const double log_s = log(S), lse = (double)m + log_s;
   if (lane == 0) {
     if (a.logprob) a.logprob[r] = (float)(z_s[NC] - lse);
     if (a.entropy) a.entropy[r] = (float)(log_s - T / S);
   }
-  // ---- order: rank of each candidate by (logit, lower index first)
-  if (lane < NC) {
-    const double z = z_s[lane];
-    const int v = id_s[lane];
-    int rank = 0;
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      if (k == lane) continue;
-      // candidates that are missing (fewer logits above -inf than asked for) come last, in list order
-      const bool ahead = id_s[k] < 0 ? (v < 0 && k < lane) : (v < 0 || z_s[k] > z || (z_s[k] == z && id_s[k] < v));
-      rank += ahead;
-    }
-    if (rank < a.n_top) {
-      a.top_ids[(size_t)r * a.n_top + rank] = v;
-      a.top_logprobs[(size_t)r * a.n_top + rank] = (float)(z - lse);
-    }
+  if (lane < NC && rank_s[lane] < a.n_top) {
+    a.top_ids[(size_t)r * a.n_top + rank_s[lane]] = id_s[lane];
+    a.top_logprobs[(size_t)r * a.n_top + rank_s[lane]] = (float)(z_s[lane] - lse);
   }
 }
 
