@@ -609,23 +609,41 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
     const KaPlace e = edge[side];
     const int c0 = ends[side][0], c1 = ends[side][1];
     const int n_q = span[e.b].w * group;
-    for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
-      const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
-      float mm = -INFINITY, ls = 0.0f;
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // a thread's items (row, 4 dimensions) side by side, so that the partials of one CTA are one round trip
+    constexpr int kItems = cdiv(8 * NT * (DIM / 4), kThreads);
+    float mm[kItems], ls[kItems];
+    float4 acc[kItems];
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+      mm[u] = -INFINITY, ls[u] = 0.0f;
+      acc[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
 #pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const float* x = a.part + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * (8 * NT) + r) * (DIM + 2);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(x + DIM));
-        const float2 v0 = __ldcg(reinterpret_cast<const float2*>(x + d)), v1 = __ldcg(reinterpret_cast<const float2*>(x + d + 2));
-        const float now = fmaxf(mm, ml.x), base = now > -INFINITY ? now : 0.0f;
-        const float f = ex2(mm - base), h = ex2(ml.x - base);
-        mm = now;
-        ls = ls * f + ml.y * h;
-        acc.x = acc.x * f + v0.x * h, acc.y = acc.y * f + v0.y * h;
-        acc.z = acc.z * f + v1.x * h, acc.w = acc.w * f + v1.y * h;
+    for (int c = c0; c <= c1; ++c) {
+      const float* part = a.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * (8 * NT) * (DIM + 2);
+      float2 ml[kItems], v0[kItems], v1[kItems];
+#pragma unroll
+      for (int u = 0; u < kItems; ++u) {
+        const int i = min(tid + u * kThreads, 8 * NT * (DIM / 4) - 1);
+        const float* x = part + i / (DIM / 4) * (DIM + 2);
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(x + DIM));
+        v0[u] = __ldcg(reinterpret_cast<const float2*>(x + i % (DIM / 4) * 4));
+        v1[u] = __ldcg(reinterpret_cast<const float2*>(x + i % (DIM / 4) * 4 + 2));
       }
-      ka_store<DIM, NT>(a, e, n_q, r, d, acc, ls);
+#pragma unroll
+      for (int u = 0; u < kItems; ++u) {
+        const float now = fmaxf(mm[u], ml[u].x), base = now > -INFINITY ? now : 0.0f;
+        const float f = ex2(mm[u] - base), h = ex2(ml[u].x - base);
+        mm[u] = now;
+        ls[u] = ls[u] * f + ml[u].y * h;
+        acc[u].x = acc[u].x * f + v0[u].x * h, acc[u].y = acc[u].y * f + v0[u].y * h;
+        acc[u].z = acc[u].z * f + v1[u].x * h, acc[u].w = acc[u].w * f + v1[u].y * h;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+      const int i = tid + u * kThreads;
+      if (i < 8 * NT * (DIM / 4)) ka_store<DIM, NT>(a, e, n_q, i / (DIM / 4), i % (DIM / 4) * 4, acc[u], ls[u]);
     }
     if (tid == 0) atomicExch(a.arrived + c0, 0u);
   }
