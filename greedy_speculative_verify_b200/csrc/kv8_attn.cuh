@@ -20,23 +20,28 @@
 // Work: a unit is (sequence, kv head, 8 NT query rows), cut into tiles of 16
 // positions a warp. All tiles of the batch form one list, of which every CTA
 // takes an equal contiguous share, whatever the lengths are. Warp w runs its own
-// softmax over positions 16 w .. 16 w + 15 of every tile, straight out of
-// registers: 16-byte loads, the next tile's keys requested as soon as this
-// tile's are used up, and its values likewise. At a unit's end the warps are
-// merged in shared memory. A unit that lies in several CTAs' shares leaves
-// partials, which the last of them to finish merges in CTA order, so results do
-// not depend on timing.
+// softmax over positions 16 w .. 16 w + 15 of every tile. Its codes come by 16-byte
+// asynchronous copies into its own place in shared memory: a lane reads what it
+// copied itself, so there is no barrier, and requests the next tile's keys as soon
+// as this tile's are read, its values likewise. At a unit's end the warps are merged
+// in shared memory. A unit that lies in several CTAs' shares leaves partials, which
+// the last of them to finish merges in CTA order, so results do not depend on
+// timing.
 //
 // Bound by HBM where caches are long: 16 sequences x 10 heads at 32,760 positions,
-// 8 rows each, 205 us for 1.34 GB (6.5 TB/s, what a copy reaches). At 2,048
-// positions (32 sequences, 1,650 on average, 135 MB) 33 us against 21: about 5 us
-// until every SM has its first tile, 14 tiles of 1.2 us, 1.5 us a unit's turn, 4 us
-// for the units that CTAs share. With 16 rows to a kv head (32 heads on 8, 491 MB)
-// 109 us against 75: 12 warps an SM wait for their own chains of products. Feeding
-// the warps through shared memory instead (bulk copies by a producer warp, rings
-// of their own, or 16-byte asynchronous copies) took 264, 350 and 235 us where
-// this takes 205: the same loads plus the instructions to wait for and re-read
-// them; requesting tiles into L2 ahead of time changed nothing.
+// 8 rows each, 200 us for 1.34 GB (6.7 TB/s, what a copy reaches). At 2,048
+// positions (32 sequences, 1,650 on average, 135 MB) 32 us against 21: about 5 us
+// until every SM has its first tile, the turns from unit to unit, 4 us for the units
+// that CTAs share. With 16 rows to a kv head (32 heads on 8, 491 MB) 91 us against
+// 75, with 32 rows 154: 12 warps an SM wait for their own chains of products. One
+// sequence of 777 positions: 9.7 us, of which the tile itself is 2; 3,000: 14.7, with
+// 47 partials a unit to join.
+// Loads into registers instead of the copies: 104.6 and 188.5 us where these take
+// 91 and 154 (the 32 registers they free are what the loop waits for), 205 where
+// these take 200. The copies go by way of L1, and the rest of L1 matters to them: a
+// larger part of it given to shared memory, or more tiles a warp under way, took 105
+// to 108 us; past L1 (.cg) 108. Bulk copies by a producer warp, or rings that a warp
+// shares, took 264 and 350 us at 32,760 positions: their barriers.
 #pragma once
 #include "attention.cuh"
 #include "kv8.cuh"
@@ -45,7 +50,7 @@ namespace vg {
 
 constexpr int kKaMaxRows = 8;      // new rows per sequence
 constexpr int kKaMaxGroup = 16;    // query heads per kv head
-constexpr int kKaTable = 512;      // sequences per launch
+constexpr int kKaTable = 128;      // sequences per launch
 constexpr float kKaSlack = 6.0f;   // log2 of the largest weight
 constexpr float kKaLift = 512.0f;  // 2^9, on the f16 weights
 constexpr float kKaTiny = 5.9604645e-8f;  // 2^-24, the unit of f16 subnormals
@@ -60,17 +65,22 @@ struct Kv8AttnArgs {
   const int32_t* first;  // [B] or null: 0
   const int32_t* n_new;  // [B] or null: all rows
   float scale_log2;      // scale * log2(e) / Q
-  float* part;           // [2 grid][8 NT][DIM + 2]: weighted values, then maximum and sum
+  float* part;           // [2 grid][8 NT][DIM + 4]: weighted values, then maximum and sum
   uint32_t* arrived;     // [grid]: partials written of the unit that starts in CTA i and ends in a later one; zero between calls
   __nv_bfloat16* o;
   int64_t o_stride;
 };
 
 // Warps per CTA and CTAs per SM: 16 warps of at most 128 registers where a unit
-// has up to 8 query rows (as 4 x 4 instead of 8 x 2: 36.0 us where this takes
-// 33.4), 12 of at most 168 where it has 16 (8 of 240: 120 us where this takes 109).
-__host__ __device__ constexpr int ka_warps(int nt) { return nt == 1 ? 8 : 4; }
-__host__ __device__ constexpr int ka_ctas(int nt) { return nt == 1 ? 2 : 3; }
+// has up to 8 query rows, 12 of at most 168 where it has 16 (8 of 240: 120 us where
+// 12 took 109). Small CTAs: their turns from unit to unit fall apart in time (8
+// warps x 2: 33.4 us where 4 x 4 takes 32.2).
+constexpr int kKaWarps = 4;
+__host__ __device__ constexpr int ka_ctas(int nt) { return nt == 1 ? 4 : 3; }
+// Tiles of a warp on their way to shared memory: 4 KB of codes. (Two at 128
+// dimensions: 236 us at 32,760 positions where one takes 200.)
+__host__ __device__ constexpr int ka_slots(int dim) { return dim == 128 ? 1 : 2; }
+__host__ __device__ constexpr int ka_ring_bytes(int dim) { return kKaWarps * ka_slots(dim) * 2 * kKv8Group * dim; }
 
 // m16n8k16, f16 operands, fp32 accumulators; fragments as in mma_16816.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -363,14 +373,25 @@ struct KaPlace {
   int j, n;          // tile of the unit, and how many it has
 };
 
-// 16 bytes read once: not kept in L1.
-__device__ __forceinline__ uint4 ka_ld(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
+// 16 bytes global -> shared, asynchronous; groups of them complete in order. (By way
+// of L1: past it, .cg, 32 heads on 8 took 108 us where this takes 91.)
+__device__ __forceinline__ void ka_cp16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void ka_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ka_cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// A lane's 16 bytes of every 512 from p on.
+template <int N>
+__device__ __forceinline__ void ka_lds(uint4 (&v)[N], uint32_t p) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w)
+                 : "r"(p + j * 512)
+                 : "memory");
 }
 
 // o of row r of p's tile, dimensions d .. d + 3, from the weighted values and the
@@ -388,10 +409,13 @@ __device__ __forceinline__ void ka_store(const Kv8AttnArgs& a, const KaPlace& p,
 }
 
 template <int FMT, int DIM, int NT>
-__global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const Kv8AttnArgs a) {
-  constexpr int W = ka_warps(NT), kThreads = 32 * W, kTile = kKv8Group * W, kRowW = DIM + 4;
-  __shared__ __align__(16) float wo[W * 8 * NT * kRowW];
-  __shared__ float wm[W * 8 * NT], wl[W * 8 * NT];
+__global__ void __launch_bounds__(32 * kKaWarps, ka_ctas(NT)) kv8_attn(const Kv8AttnArgs a) {
+  constexpr int W = kKaWarps, kThreads = 32 * W, kTile = kKv8Group * W;
+  constexpr int kRowW = DIM + 4, kPartW = DIM + 4;  // floats of a row: of a warp's sums, of a CTA's partials
+  constexpr int S = ka_slots(DIM), kHalf = kKv8Group * DIM, kSlot = 2 * kHalf;  // a slot: a group's keys, its values
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ __align__(16) float wo[W * 8 * kRowW];
+  __shared__ float wm[W * 8], wl[W * 8];
   __shared__ Kv8Rows<DIM, NT> rows_s;  // (unused with one tile of rows)
   __shared__ int start[kKaTable + 1];  // first tile of each sequence
   __shared__ int4 span[kKaTable];      // lo, hi, L, n
@@ -471,59 +495,72 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
   float ks = 0.0f, vs = 0.0f;
   KaPlace p = locate(t0);
   Kv8Span s;
-  const uint8_t *kp, *vp;
-  const float *ka, *va;
-  int p0;
-  auto load_k = [&]() {
+  const uint32_t ring = smem_u32(ring_smem) + warp * S * kSlot + lane * 16;  // this lane's 16 bytes of every 512
+  const uint8_t *kp = nullptr, *vp = nullptr;  // this lane's bytes of the next keys and values to request
+  const float *ka = nullptr, *va = nullptr;
+  int p0 = 0, mine = 0;  // this warp's first position, and its groups of the share of the unit
+  auto load_k = [&](int slot) {
 #pragma unroll
-    for (int h = 0; h < DIM / 64; ++h) {
-      kf[2 * h] = ka_ld(kp + h * 1024);
-      kf[2 * h + 1] = ka_ld(kp + h * 1024 + 128);
-    }
-  };
-  auto load_v = [&]() {
+    for (int h = 0; h < DIM / 64; ++h)
 #pragma unroll
-    for (int j = 0; j < DIM / 32; ++j) vf[j] = ka_ld(vp + j * 512);
+      for (int i = 0; i < 2; ++i) ka_cp16(ring + slot * kSlot + (2 * h + i) * 512, kp + h * 1024 + i * 128);
+    kp += kTile * DIM;
   };
-  auto enter = [&]() {  // a unit's share: request its query rows, then its first tile
+  auto load_v = [&](int slot) {
+#pragma unroll
+    for (int j = 0; j < DIM / 32; ++j) ka_cp16(ring + slot * kSlot + kHalf + j * 512, vp + j * 512);
+    vp += kTile * DIM;
+  };
+  auto magnitudes = [&](int p) {
+    ks = ka[p >> a.c.log2];
+    vs = va[p >> a.c.log2];
+  };
+  auto enter = [&](int T) {  // a unit's share from tile T on: request its query rows, then its first tiles
     const int4 sp = span[p.b];
     s = Kv8Span{sp.z, sp.x, sp.y, sp.w};
     if (NT == 1 || warp < NT) w.load(a, a.b0 + p.b, p.kvh, p.tile * NT + (NT == 1 ? 0 : warp), s.n * group, lane);
     p0 = s.lo / kKv8Group * kKv8Group + p.j * kTile + warp * kKv8Group;
+    mine = p0 < s.hi ? min(min(p.n - p.j, t1 - T), cdiv(s.hi - p0, kTile)) : 0;
     const size_t head = (size_t)(a.b0 + p.b) * a.c.n_kv + p.kvh;
     kp = a.c.k + (head * a.c.L_max + p0) * DIM + k_at;
     vp = a.c.v + (head * a.c.L_max + p0) * DIM + v_at;
     ka = a.c.k_amax + head * blocks, va = a.c.v_amax + head * blocks;
-    if (p0 < s.hi) {
-      ks = ka[p0 >> a.c.log2];
-      vs = va[p0 >> a.c.log2];
-      load_k();
-      load_v();
+    if (mine > 0) magnitudes(p0);
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      if (i < mine) load_k(i);
+      ka_cp_commit();
+      if (i < mine) load_v(i);
+      ka_cp_commit();
     }
   };
-  enter();
+  enter(t0);
   for (int T = t0; T < t1;) {
     const int seg0 = T - p.j, seg1 = seg0 + p.n;  // the unit's tiles
     const int n = min(seg1, t1) - T;              // those of this CTA
     w.begin(a, p.tile, s, warp, lane, &rows_s);
-    for (int i = 0; i < n && p0 < s.hi; ++i) {
-      const bool more = i + 1 < n && p0 + kTile < s.hi;
+    int slot = 0;
+    for (int i = 0; i < mine; ++i) {
+      const bool more = i + S < mine;  // another tile to request
       float z[NT][4];
       uint32_t b0[NT], b1[NT];
+      // a lane reads what it copied itself, and requests the next 16 bytes into the
+      // same place: no barrier. Copies complete in the order K0 V0 K1 V1 ..; 2 S are
+      // under way (empty ones at the end), the oldest is wanted.
+      ka_cp_wait<2 * S - 1>();
+      ka_lds(kf, ring + slot * kSlot);
       w.scores(kf, z, &rows_s, lane);
       const float ks_now = ks, vs_now = vs;
-      if (more) {
-        kp += kTile * DIM;
-        load_k();
-        ks = ka[(p0 + kTile) >> a.c.log2];
-        vs = va[(p0 + kTile) >> a.c.log2];
-      }
+      if (more) load_k(slot);
+      ka_cp_commit();
+      if (i + 1 < mine) magnitudes(p0 + kTile);
       w.weights(z, ks_now, vs_now, p0, s.lo, p0 >= s.lo && p0 + kKv8Group - 1 <= s.L, lane, b0, b1);
+      ka_cp_wait<2 * S - 1>();
+      ka_lds(vf, ring + slot * kSlot + kHalf);
       w.values(vf, b0, b1, s.hi - p0, lane);
-      if (more) {
-        vp += kTile * DIM;
-        load_v();
-      }
+      if (more) load_v(slot);
+      ka_cp_commit();
+      if (++slot == S) slot = 0;
       p0 += kTile;
     }
     T += n;
@@ -534,54 +571,56 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
       if (T == t1) edge[1] = p;
     }
     const int n_q = s.n * group;
-    // ---- merge the warps: their sums to shared memory
+    // ---- merge the warps, 8 rows at a time: their sums to shared memory, then a thread per row and 4 dimensions
     const float back = w.top_v / (kv8_q<FMT>() * kKaLift);
+    float* slot_out = a.part + (size_t)(2 * me + (seg0 < t0 ? 0 : 1)) * (8 * NT) * kPartW;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt > 0) __syncthreads();
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = nt * 8 + 2 * t + e;
+        const int r = 2 * t + e;
         float l = w.l[nt][e];
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         if (g == 0) {
-          wm[warp * 8 * NT + r] = w.m[nt][e];
-          wl[warp * 8 * NT + r] = l;
+          wm[warp * 8 + r] = w.m[nt][e];
+          wl[warp * 8 + r] = l;
         }
 #pragma unroll
         for (int j = 0; j < DIM / 32; ++j)
-          *reinterpret_cast<float4*>(wo + (warp * 8 * NT + r) * kRowW + 4 * (g + 8 * j)) =
+          *reinterpret_cast<float4*>(wo + (warp * 8 + r) * kRowW + 4 * (g + 8 * j)) =
               make_float4(w.o[nt][j][0][e] * back, w.o[nt][j][0][2 + e] * back, w.o[nt][j][1][e] * back,
                           w.o[nt][j][1][2 + e] * back);
       }
-    if (T < t1) {  // the next unit's data travels while this one's warps are merged
-      p = place(T, p.b);
-      enter();
-    }
-    __syncthreads();
-    float* slot = a.part + (size_t)(2 * me + (seg0 < t0 ? 0 : 1)) * (8 * NT) * (DIM + 2);
-    for (int i = tid; i < 8 * NT * (DIM / 4); i += kThreads) {
-      const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
-      float mm = -INFINITY, ls = 0.0f;
-#pragma unroll
-      for (int k = 0; k < W; ++k) mm = fmaxf(mm, wm[k * 8 * NT + r]);
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (mm > -INFINITY) {
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-          const float f = ex2(wm[k * 8 * NT + r] - mm);
-          const float4 v = *reinterpret_cast<const float4*>(wo + (k * 8 * NT + r) * kRowW + d);
-          ls += wl[k * 8 * NT + r] * f;
-          acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
-        }
+      if (nt == NT - 1 && T < t1) {  // the next unit's data travels while this one's warps are merged
+        p = place(T, p.b);
+        enter(T);
       }
-      if (whole) {
-        ka_store<DIM, NT>(a, done, n_q, r, d, acc, ls);
-      } else {
-        *reinterpret_cast<float2*>(slot + r * (DIM + 2) + d) = make_float2(acc.x, acc.y);
-        *reinterpret_cast<float2*>(slot + r * (DIM + 2) + d + 2) = make_float2(acc.z, acc.w);
-        if (d == 0) *reinterpret_cast<float2*>(slot + r * (DIM + 2) + DIM) = make_float2(mm, ls);
+      __syncthreads();
+      for (int i = tid; i < 8 * (DIM / 4); i += kThreads) {
+        const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
+        float mm = -INFINITY, ls = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) mm = fmaxf(mm, wm[k * 8 + r]);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (mm > -INFINITY) {
+#pragma unroll
+          for (int k = 0; k < W; ++k) {
+            const float f = ex2(wm[k * 8 + r] - mm);
+            const float4 v = *reinterpret_cast<const float4*>(wo + (k * 8 + r) * kRowW + d);
+            ls += wl[k * 8 + r] * f;
+            acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+          }
+        }
+        if (whole) {
+          ka_store<DIM, NT>(a, done, n_q, nt * 8 + r, d, acc, ls);
+        } else {
+          float* x = slot_out + (nt * 8 + r) * kPartW;
+          *reinterpret_cast<float4*>(x + d) = acc;
+          if (d == 0) *reinterpret_cast<float2*>(x + DIM) = make_float2(mm, ls);
+        }
       }
     }
     __syncthreads();  // the merge buffers are free again
@@ -609,8 +648,13 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
     const KaPlace e = edge[side];
     const int c0 = ends[side][0], c1 = ends[side][1];
     const int n_q = span[e.b].w * group;
-    // a thread's items (row, 4 dimensions) side by side, so that the partials of one CTA are one round trip
-    constexpr int kItems = cdiv(8 * NT * (DIM / 4), kThreads);
+    // A row belongs to kLanes lanes, 4 dimensions each. They take as many CTAs'
+    // partials at a time: their maxima and sums a lane each, then the values, 8
+    // requests of 16 bytes under way. (4: 47 partials take 3.6 us longer; 16: the
+    // registers cost the main loop 1.3 us at 32 sequences of 2,048 positions.)
+    constexpr int kLanes = DIM / 4, kItems = 8 * NT * kLanes / kThreads, kBatch = 8 / kItems;
+    static_assert(kLanes <= 32 && kLanes % kBatch == 0 && kItems * kThreads == 8 * NT * kLanes);
+    const int sub = tid % kLanes, r0 = tid / kLanes;  // rows r0 + u * (kThreads / kLanes)
     float mm[kItems], ls[kItems];
     float4 acc[kItems];
 #pragma unroll
@@ -618,33 +662,55 @@ __global__ void __launch_bounds__(32 * ka_warps(NT), ka_ctas(NT)) kv8_attn(const
       mm[u] = -INFINITY, ls[u] = 0.0f;
       acc[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float* part = a.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * (8 * NT) * (DIM + 2);
-      float2 ml[kItems], v0[kItems], v1[kItems];
+#pragma unroll 1
+    for (int c = c0; c <= c1; c += kLanes) {
+      const int nc = min(kLanes, c1 + 1 - c);
+      auto row = [&](int j, int u) {  // row u of this thread in the partials of CTA c + j
+        const int slot = 2 * (c + j) + (c + j == c0 ? 1 : 0);
+        return a.part + ((size_t)slot * (8 * NT) + r0 + u * (kThreads / kLanes)) * kPartW;
+      };
+      float2 ml[kItems];
+      float f[kItems];
 #pragma unroll
-      for (int u = 0; u < kItems; ++u) {
-        const int i = min(tid + u * kThreads, 8 * NT * (DIM / 4) - 1);
-        const float* x = part + i / (DIM / 4) * (DIM + 2);
-        ml[u] = __ldcg(reinterpret_cast<const float2*>(x + DIM));
-        v0[u] = __ldcg(reinterpret_cast<const float2*>(x + i % (DIM / 4) * 4));
-        v1[u] = __ldcg(reinterpret_cast<const float2*>(x + i % (DIM / 4) * 4 + 2));
-      }
+      for (int u = 0; u < kItems; ++u)
+        ml[u] = sub < nc ? __ldcg(reinterpret_cast<const float2*>(row(sub, u) + DIM)) : make_float2(-INFINITY, 0.0f);
+#pragma unroll 1
+      for (int j0 = 0; j0 < nc; j0 += kBatch) {
+        float4 v[kBatch][kItems];
 #pragma unroll
-      for (int u = 0; u < kItems; ++u) {
-        const float now = fmaxf(mm[u], ml[u].x), base = now > -INFINITY ? now : 0.0f;
-        const float f = ex2(mm[u] - base), h = ex2(ml[u].x - base);
-        mm[u] = now;
-        ls[u] = ls[u] * f + ml[u].y * h;
-        acc[u].x = acc[u].x * f + v0[u].x * h, acc[u].y = acc[u].y * f + v0[u].y * h;
-        acc[u].z = acc[u].z * f + v1[u].x * h, acc[u].w = acc[u].w * f + v1[u].y * h;
+        for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+          for (int u = 0; u < kItems; ++u)
+            if (j0 + j < nc) v[j][u] = __ldcg(reinterpret_cast<const float4*>(row(j0 + j, u) + 4 * sub));
+        if (j0 == 0) {
+#pragma unroll
+          for (int u = 0; u < kItems; ++u) {
+            float now = ml[u].x;
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+            now = fmaxf(now, mm[u]);
+            const float base = now > -INFINITY ? now : 0.0f, back = ex2(mm[u] - base);
+            f[u] = ex2(ml[u].x - base);
+            float l = ml[u].y * f[u];
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            mm[u] = now;
+            ls[u] = ls[u] * back + l;
+            acc[u].x *= back, acc[u].y *= back, acc[u].z *= back, acc[u].w *= back;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+          for (int u = 0; u < kItems; ++u) {
+            const float h = __shfl_sync(0xffffffffu, f[u], j0 + j, kLanes);
+            if (j0 + j < nc)
+              acc[u].x += v[j][u].x * h, acc[u].y += v[j][u].y * h, acc[u].z += v[j][u].z * h, acc[u].w += v[j][u].w * h;
+          }
       }
     }
 #pragma unroll
-    for (int u = 0; u < kItems; ++u) {
-      const int i = tid + u * kThreads;
-      if (i < 8 * NT * (DIM / 4)) ka_store<DIM, NT>(a, e, n_q, i / (DIM / 4), i % (DIM / 4) * 4, acc[u], ls[u]);
-    }
+    for (int u = 0; u < kItems; ++u) ka_store<DIM, NT>(a, e, n_q, r0 + u * (kThreads / kLanes), 4 * sub, acc[u], ls[u]);
     if (tid == 0) atomicExch(a.arrived + c0, 0u);
   }
 }

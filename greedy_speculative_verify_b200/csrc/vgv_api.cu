@@ -33,7 +33,7 @@ namespace {
 constexpr int kH = 1280, kI = 896, kE = 64, kS = 2, kTopK = 6;
 constexpr int kMaxDevices = 64;
 constexpr int kMaxSmemBytes = 232448;  // shared memory a CTA can ask for (227 KB)
-constexpr int kKaMaxGrid = 512;     // CTAs of the 8-bit attention kernel at most
+constexpr int kKaMaxGrid = 1024;    // CTAs of the 8-bit attention kernel at most
 constexpr int kEntryMaxGrid = 256;  // CTAs of the layer-entry kernel at most
 
 // Bytes of expert weights the layer entry prefetches into L2: the gate|up rows
@@ -157,6 +157,10 @@ vg_status device_state(DevState** out) {
       if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
               cudaSuccess)
+        return cuda_fail();
+    for (auto* k : {vg::kv8_attn<0, 64, 1>, vg::kv8_attn<0, 64, 2>, vg::kv8_attn<0, 128, 1>, vg::kv8_attn<0, 128, 2>,
+                    vg::kv8_attn<1, 64, 1>, vg::kv8_attn<1, 64, 2>, vg::kv8_attn<1, 128, 1>, vg::kv8_attn<1, 128, 2>})
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, vg::ka_ring_bytes(128)) != cudaSuccess)
         return cuda_fail();
     // Kernels that follow each other with dependent launches share SMs only if
     // their shared-memory configurations agree: every kernel of the decode
@@ -1347,7 +1351,7 @@ KaWs kv8_attn_layout(const vg_kv8* c, int rows, int n_heads) {
   KaWs L{};
   L.arrived = 0;
   L.part = align256((size_t)kKaMaxGrid * 4);
-  L.total = L.part + align256((size_t)2 * kKaMaxGrid * 8 * nt * (c->dim + 2) * 4);
+  L.total = L.part + align256((size_t)2 * kKaMaxGrid * 8 * nt * (c->dim + 4) * 4);
   return L;
 }
 size_t kv8_attn_ws(const vg_kv8* c, int rows, int n_heads) { return kv8_attn_layout(c, rows, n_heads).total; }
@@ -1407,16 +1411,16 @@ vg_status kv8_attn_launch(DevState* dev, const vg_kv8* c, int32_t rows, int32_t 
   a.o = static_cast<__nv_bfloat16*>(o);
   a.o_stride = o_stride;
   // sequences per launch: what the kernel's table holds, and no more than 2^30 tiles
-  const int64_t tiles = (int64_t)c->n_kv * a.n_tiles * (cdiv(c->L_max, kKv8Group * ka_warps(nt)) + 1);
+  const int64_t tiles = (int64_t)c->n_kv * a.n_tiles * (cdiv(c->L_max, kKv8Group * kKaWarps) + 1);
   const int per = (int)max((int64_t)1, min((int64_t)kKaTable, ((int64_t)1 << 30) / tiles));
   for (a.b0 = 0; a.b0 < c->B; a.b0 += per) {
     a.nb = min(per, c->B - a.b0);
-    const int grid = min(dev->sms * ka_ctas(nt), kKaMaxGrid), threads = 32 * ka_warps(nt);
+    const int grid = min(dev->sms * ka_ctas(nt), kKaMaxGrid), threads = 32 * kKaWarps;
     ProfScope ps(VG_KERNEL_ATTENTION, s);
     const cudaError_t e = kv8_dispatch(c->format, c->dim, [&](auto fmt, auto dim) {
       constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
-      return nt == 1 ? launch_dep(kv8_attn<F, D, 1>, grid, threads, 0, s, Launch::kPlain, a)
-                     : launch_dep(kv8_attn<F, D, 2>, grid, threads, 0, s, Launch::kPlain, a);
+      return nt == 1 ? launch_dep(kv8_attn<F, D, 1>, grid, threads, ka_ring_bytes(D), s, Launch::kPlain, a)
+                     : launch_dep(kv8_attn<F, D, 2>, grid, threads, ka_ring_bytes(D), s, Launch::kPlain, a);
     });
     if (e != cudaSuccess) return cuda_fail();
   }

@@ -494,10 +494,10 @@ vg_status vg_kv8_read(const vg_kv8* c, int32_t rows, const int32_t* pos, const i
  * rounded to 2^-11 of themselves (those that, times their block's share of the
  * largest value magnitude, are below 2^-23: to 2^-34); sums and maxima are
  * fp32, o is rounded once.
- * One launch for every 512 sequences. workspace: vg_kv8_attn_workspace_bytes(c,
+ * One launch for every 128 sequences. workspace: vg_kv8_attn_workspace_bytes(c,
  * rows, n_heads) bytes, 16-byte aligned, ZERO-FILLED before its first call;
  * every call leaves its counters zero again, so later calls (one at a time) need
- * no clearing, unless one recorded VG_ERR_TIMEOUT. Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED (rows > 8, more than
+ * no clearing. Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED (rows > 8, more than
  * 16 query heads to a key/value head), VG_ERR_WORKSPACE, VG_ERR_CUDA. */
 size_t vg_kv8_attn_workspace_bytes(const vg_kv8* c, int32_t rows, int32_t n_heads);
 vg_status vg_kv8_attn(const vg_kv8* c, int32_t rows, int32_t n_heads, const void* q, int64_t q_stride,
@@ -508,8 +508,9 @@ vg_status vg_kv8_attn(const vg_kv8* c, int32_t rows, int32_t n_heads, const void
  * the cache's): the same layer, with the new rows' k (rotated) and v quantised
  * into the cache (vg_kv8_append at positions lens[b] ..) and the rows' attention
  * read from it (vg_kv8_attn, scale 1/sqrt(128); the workspace is zero-filled
- * before its first call, as there). Arguments and errors otherwise as there; unlike there, an overflowing sequence's two device errors share the
- * status word. */
+ * before its first call, as there). Arguments and errors otherwise as there;
+ * unlike there, an overflowing sequence's two device errors share the status
+ * word. */
 size_t vg_attn_verify_kv8_workspace_bytes(const vg_kv8* c, int32_t K);
 vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* x, const void* w_qkv, const void* w_o,
                              const int32_t* lens, void* out, void* o_out, void* workspace, size_t workspace_bytes,
