@@ -379,13 +379,14 @@ def _need(ok, what):
 
 
 def _same_device(device, *tensors):
-    """Every tensor lies on `device`, and if that is a CUDA device it is the
-    current one: the library launches on the current device."""
+    """Every tensor lies on `device`, a CUDA device and the current one: the
+    library launches there, and its kernels take the addresses as they are."""
     for t in tensors:
         if t is not None and t.device != device:
             raise ValueError(f"a tensor is on {t.device}, not on {device}")
-    index = device.index
-    if index is not None and index != _t().cuda.current_device():
+    if device.type != "cuda":
+        raise ValueError(f"tensors are on {device}, not on a CUDA device")
+    if device.index != _t().cuda.current_device():
         raise ValueError(f"tensors are on {device}, which is not the current device")
 
 

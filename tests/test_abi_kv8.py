@@ -139,3 +139,16 @@ def test_binding_refuses_wrong_tensors():
               lambda: vgv.vg_token_logprobs(bf(2, 64).T.contiguous().T, bf(9, 64), i, None, None, None, None, ws)):
         with pytest.raises(ValueError):
             f()
+
+
+def test_binding_refuses_host_tensors():
+    """Tensors that lie in host memory: a kernel would take their addresses as they are."""
+    k, a = torch.zeros(2, 3, 64, 64, dtype=torch.int8), torch.zeros(2, 3, 4)
+    c = vgv.make_kv8(k, k.clone(), a, a.clone())
+    x, i, ws = torch.zeros(8, 192, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32), torch.zeros(1 << 16, dtype=torch.uint8)
+    h, f = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(2)
+    for call in (lambda: vgv.vg_kv8_append(c, 4, x, x.clone(), i), lambda: vgv.vg_kv8_read(c, 4, i, x, None),
+                 lambda: vgv.vg_kv8_attn(c, 4, 3, x, i, 0.1, x.clone(), ws),
+                 lambda: vgv.vg_token_logprobs(h, h.clone(), i, f, None, None, None, ws)):
+        with pytest.raises(ValueError, match="not on a CUDA device"):
+            call()
