@@ -605,14 +605,13 @@ __global__ void __launch_bounds__(32 * kKaWarps, ka_ctas(NT)) kv8_attn(const Kv8
 #pragma unroll
         for (int k = 0; k < W; ++k) mm = fmaxf(mm, wm[k * 8 + r]);
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (mm > -INFINITY) {
+        const float base = mm > -INFINITY ? mm : 0.0f;  // (a row of NaN has no maximum and keeps its NaN)
 #pragma unroll
-          for (int k = 0; k < W; ++k) {
-            const float f = ex2(wm[k * 8 + r] - mm);
-            const float4 v = *reinterpret_cast<const float4*>(wo + (k * 8 + r) * kRowW + d);
-            ls += wl[k * 8 + r] * f;
-            acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
-          }
+        for (int k = 0; k < W; ++k) {
+          const float f = ex2(wm[k * 8 + r] - base);
+          const float4 v = *reinterpret_cast<const float4*>(wo + (k * 8 + r) * kRowW + d);
+          ls += wl[k * 8 + r] * f;
+          acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
         }
         if (whole) {
           ka_store<DIM, NT>(a, done, n_q, nt * 8 + r, d, acc, ls);

@@ -488,7 +488,7 @@ vg_status vg_kv8_read(const vg_kv8* c, int32_t rows, const int32_t* pos, const i
  * none) are not read and get o = 0. lens[b] < 0, first[b] < 0, n_new[b] outside
  * [0, rows] or lens[b] + n_new[b] > L_max records VG_ERR_DEVICE_BOUNDS and gives
  * o = 0 for that sequence. scale > 0; of a row with scores beyond the fp32
- * range nothing is promised.
+ * range nothing is promised; a row with a NaN gives NaN, unless it sees nothing.
  * Precision: codes enter both products exactly (f16 operands, fp32 sums), query
  * rows exactly down to 2^-29 of their largest element; softmax weights are
  * rounded to 2^-11 of themselves (those that, times their block's share of the

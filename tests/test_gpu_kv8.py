@@ -329,6 +329,32 @@ def test_attention_extreme_scores(fmt):
         check_attention(d, 2, 2, [200, 77], scale=scale)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("group", [1, 4])
+def test_attention_nan_query(fmt, group):
+    """A query row with a NaN gives NaN there, whether one CTA holds its unit or
+    several, and changes no bit of the other rows; a row that sees nothing
+    stays 0."""
+    c = Cache(fmt, 3, 2, 2048, 128, 64, seed=17)
+    rows, w = 4, 2 * group * 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn(12, w, generator=g, device="cuda").bfloat16()
+    bad = q.clone()
+    bad[1, 130] = bad[6, 5] = bad[8, 7] = float("nan")  # the last of a row that sees nothing
+    lens, first = i32([2000, 30, 9]), i32([0, 0, 10])
+    ws = torch.zeros(vgv.vg_kv8_attn_workspace_bytes(c.h, rows, 2 * group), dtype=torch.uint8, device="cuda")
+    o = [torch.zeros_like(q) for _ in "ab"]
+    for x, y in zip((q, bad), o):
+        vgv.vg_kv8_attn(c.h, rows, 2 * group, x, lens, 0.1, y, ws, first=first)
+    ok()
+    hit = torch.zeros(12, 2 * group, dtype=torch.bool, device="cuda")
+    hit[1, 1] = hit[6, 0] = True
+    nan = o[1].view(12, 2 * group, 128).isnan()
+    assert torch.equal(nan, hit[:, :, None].expand_as(nan))
+    assert torch.equal(o[0].view_as(nan)[~nan], o[1].view_as(nan)[~nan])
+    assert not o[1][8].any()
+
+
 def test_attention_value_scales_far_apart():
     """Neighbouring blocks whose value magnitudes differ by 2^40, rising and falling."""
     c = Cache("int8", 2, 1, 256, 128, 16, seed=12)

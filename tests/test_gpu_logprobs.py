@@ -92,6 +92,13 @@ def test_logprobs(R, H, V, n_top):
     check(h, lm, tok, n_top)
 
 
+@pytest.mark.parametrize("R,V,n_top", [(300, 20, 20), (129, 1, 1), (512, 130, 4), (257, 256, 8)])
+def test_many_rows_few_tokens(R, V, n_top):
+    """Vocabularies of one tile, down to one that leaves a pair's second half empty."""
+    h, lm, tok = inputs(R, 64, V, seed=R + V, sure=4.0)
+    check(h, lm, tok, n_top)
+
+
 def test_full_vocabulary():
     h, lm, tok = inputs(8, DIMS.H, DIMS.V, seed=5, sure=14.0)
     check(h, lm, tok, 20)
