@@ -18,10 +18,9 @@
 // depend on the tensor cores' summation; kLpSpare or more candidates beyond n
 // keep one from being lost to fp32 rounding at the border.
 //
-// Up to 128 rows the LM head's stream bounds it: 62 us for 4 rows (331 MB: 50.4 at
-// copy speed), of which 8 are the finishing kernel's round trips, 78 us for 128
-// rows with 20 alternatives, whose insertions into lists of 24 (in the first tile
-// nearly half of the columns enter) outlast a tile's arrival. 4,096 rows: 1.04 to
+// Up to 128 rows the LM head's stream bounds it: 60 us for 4 rows (331 MB: 50.4 at
+// copy speed), of which 8 are the finishing kernel's round trips, 68 us for 128
+// rows with 20 alternatives, 63 with up to 8. 4,096 rows: 1.04 to
 // 1.12 ms for 1.36 TFLOP (0.82 at cuBLAS's burst rate, 0.99 at its rate under the
 // power cap), 56 us of it finishing. Two epilogue threads a row, or tensor memory
 // read a chunk ahead, changed nothing at 4,096 rows and cost 3 to 11 us at 128.
@@ -46,6 +45,7 @@ struct LpArgs {
   float* stat;                 // [n_groups][3][R]: m, S, T
   unsigned long long* cand;    // [n_groups][R][NC]: order-preserving keys, descending; 0 = none
   uint32_t* floor;             // [R] or null: order-preserving image of a logit that NC others reach (0: none known)
+  uint32_t* peaks;             // [NC][128] or null: images of the largest logits of NC parts of the vocabulary; zero between calls
 };
 
 // b_rows: vocabulary rows of a tile that one CTA holds
@@ -310,8 +310,7 @@ __global__ void __launch_bounds__(192, 1)
         least = INFINITY;  // nothing enters
       } else if (a.floor) {
         const uint32_t f = *reinterpret_cast<volatile uint32_t*>(a.floor + r);
-        // a logit equal to the floor still enters: step just below it (zero: below the image of -0 too)
-        if (f > 2u) least = lp_unkey(f == 0x80000000u ? f - 2u : f - 1u);
+        if (f > 0u) least = lp_below(lp_unkey(f));
       }
       auto settle = [&]() {  // the parked columns into the list
         const int most = __reduce_max_sync(0xffffffffu, parked);
@@ -335,7 +334,7 @@ __global__ void __launch_bounds__(192, 1)
         tc_fence_after();
         const uint32_t t0 = tmem_base + ((uint32_t)(q * 32) << 16) + ab * 256;
         const int v0 = vb * a.tile_n, cols = busy ? min(a.tile_n, a.V - v0) : 0;
-        if (vb == g * a.group_tiles && __any_sync(0xffffffffu, least == -INFINITY && r < a.R)) {
+        auto own_bound = [&]() {
           // A bound to start with: NC groups of kLpBound columns have a maximum of
           // at least the NC-th largest of the groups' maxima, so NC logits reach it.
           // Finding it moves values alone (two instructions a place, and groups
@@ -363,47 +362,89 @@ __global__ void __launch_bounds__(192, 1)
           }
           least = fmaxf(least, lp_below(list.z[NC - 1]));
           list.clear();
-        }
+        };
+        // the tile's logits once: into the sums, into the lists
+        auto pass = [&](bool sums, bool lists) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < cols; c0 += kLpChunk) {
-          uint32_t zb[kLpChunk];
-          tmem_ld16(t0 + c0, zb);
-          tmem_ld_wait();
-          float z[kLpChunk], top = -INFINITY;
+          for (int c0 = 0; c0 < cols; c0 += kLpChunk) {
+            uint32_t zb[kLpChunk];
+            tmem_ld16(t0 + c0, zb);
+            tmem_ld_wait();
+            float z[kLpChunk], top = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < kLpChunk; ++j) z[j] = __uint_as_float(zb[j]);
-          if (c0 + kLpChunk > cols) {  // behind the vocabulary
+            for (int j = 0; j < kLpChunk; ++j) z[j] = __uint_as_float(zb[j]);
+            if (c0 + kLpChunk > cols) {  // behind the vocabulary
 #pragma unroll
-            for (int j = 0; j < kLpChunk; ++j)
-              if (c0 + j >= cols) z[j] = -INFINITY;
-          }
+              for (int j = 0; j < kLpChunk; ++j)
+                if (c0 + j >= cols) z[j] = -INFINITY;
+            }
 #pragma unroll
-          for (int j = 0; j < kLpChunk; ++j) top = fmaxf(top, z[j]);
-          const float now = fmaxf(m, top), base = now > -INFINITY ? now : 0.0f;
-          if (now > m && m > -INFINITY) {  // to the new maximum
-            const float d = fmaxf(m - now, -1000.0f), f = ex2(d * 1.4426950408889634f);
-            T = f * (T + S * d);
-            S *= f;
-          }
-          m = now;
-          float s1 = 0.0f, t1 = 0.0f;
-#pragma unroll
-          for (int j = 0; j < kLpChunk; ++j) {
-            const float d = z[j] - base, e = ex2(d * 1.4426950408889634f);
-            s1 += e;
-            t1 = fmaf(e, fmaxf(d, -1000.0f), t1);  // a weight of 0 adds 0, also where z is -inf
-          }
-          S += s1;
-          T += t1;
-          if (__any_sync(0xffffffffu, top > least)) {
-#pragma unroll
-            for (int j = 0; j < kLpChunk; ++j)
-              if (z[j] > least) {
-                pend[parked * kLpM + row] = make_float2(z[j], __int_as_float(v0 + c0 + j));
-                ++parked;
+            for (int j = 0; j < kLpChunk; ++j) top = fmaxf(top, z[j]);
+            if (sums) {
+              const float now = fmaxf(m, top), base = now > -INFINITY ? now : 0.0f;
+              if (now > m && m > -INFINITY) {  // to the new maximum
+                const float d = fmaxf(m - now, -1000.0f), f = ex2(d * 1.4426950408889634f);
+                T = f * (T + S * d);
+                S *= f;
               }
-            if (__any_sync(0xffffffffu, parked > kLpPend - kLpChunk)) settle();
+              m = now;
+              float s1 = 0.0f, t1 = 0.0f;
+#pragma unroll
+              for (int j = 0; j < kLpChunk; ++j) {
+                const float d = z[j] - base, e = ex2(d * 1.4426950408889634f);
+                s1 += e;
+                t1 = fmaf(e, fmaxf(d, -1000.0f), t1);  // a weight of 0 adds 0, also where z is -inf
+              }
+              S += s1;
+              T += t1;
+            }
+            if (lists && __any_sync(0xffffffffu, top > least)) {
+#pragma unroll
+              for (int j = 0; j < kLpChunk; ++j)
+                if (z[j] > least) {
+                  pend[parked * kLpM + row] = make_float2(z[j], __int_as_float(v0 + c0 + j));
+                  ++parked;
+                }
+              if (__any_sync(0xffffffffu, parked > kLpPend - kLpChunk)) settle();
+            }
           }
+        };
+        if (vb > g * a.group_tiles) {
+          pass(true, true);
+        } else if (!PAIR && a.peaks) {
+          // The first tile fixes what may enter the lists. NC parts of the
+          // vocabulary, each the groups that leave one rest by NC, have a largest
+          // logit each, so NC logits reach the smallest of those. Every CTA has its
+          // first tile at about the same time: it gives its rows' maxima away, takes
+          // the tile into the sums, and by then finds the others'. Of 129,280 tokens
+          // some 400 reach the bound then, one or two of a CTA's 880; with what a
+          // CTA's own tile shows, 70 of them entered its list of 24 (128 rows, 20
+          // alternatives: 74 us where this takes 68; 4 rows 61.4 and 59.8).
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < cols; c0 += kLpChunk) {
+            uint32_t zb[kLpChunk];
+            tmem_ld16(t0 + c0, zb);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < kLpChunk; ++j)
+              if (c0 + j < cols) top = fmaxf(top, __uint_as_float(zb[j]));
+          }
+          if (r < a.R && top > -INFINITY)
+            atomicMax(a.peaks + g % NC * kLpM + r, (uint32_t)(argmax_key(top, 0u) >> 32));
+          pass(true, false);
+          uint32_t f = 0u;
+          if (r < a.R) {
+            f = 0xFFFFFFFFu;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) f = min(f, __ldcg(a.peaks + k * kLpM + r));
+            if (f > 0u) least = lp_below(lp_unkey(f));
+          }
+          if (__any_sync(0xffffffffu, least == -INFINITY && r < a.R)) own_bound();
+          pass(false, true);
+        } else {
+          if (__any_sync(0xffffffffu, least == -INFINITY && r < a.R)) own_bound();
+          pass(true, true);
         }
         tc_fence_before();
         __syncwarp();
@@ -450,6 +491,7 @@ struct LpFinishArgs {
   float* entropy;         // [R] or null
   int32_t* top_ids;       // [R, n_top]
   float* top_logprobs;    // [R, n_top]
+  uint32_t* peaks;        // as in LpArgs
 };
 
 constexpr int kLpMaxGroups = 512;
@@ -478,6 +520,7 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (a.peaks && tid < NC) a.peaks[tid * kLpM + r] = 0u;
   const int tok = a.tokens ? a.tokens[r] : -1;
   if (tid == 0) n_pool = 0, floor_s = 1ull;  // 0 keys are no candidates
   if (tid < NC) best[tid] = 0ull, rank_s[tid] = 0;

@@ -1645,8 +1645,9 @@ LpPlan lp_plan(int R, int V, int n_top) {
   p.b_rows = p.pair ? p.tile_n / 2 : p.tile_n;
   p.stages = 8;
   while (lp_smem_bytes(p.b_rows, p.stages) > kMaxSmemBytes) --p.stages;
-  p.stat = 0;
-  p.cand = align256((size_t)p.n_groups * 3 * R * 4);
+  // the words that have to be zero between calls lie first, in every plan
+  p.stat = align256((size_t)lp_cands(kLpMaxTop) * kLpM * 4);
+  p.cand = p.stat + align256((size_t)p.n_groups * 3 * R * 4);
   p.floor = p.cand + align256((size_t)p.n_groups * R * p.n_cand * 8);
   p.total = p.floor + align256((size_t)R * 4);
   return p;
@@ -1697,6 +1698,7 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
   a.stages = p.stages;
   a.stat = reinterpret_cast<float*>(ws + p.stat);
   a.cand = reinterpret_cast<unsigned long long*>(ws + p.cand);
+  if (!p.pair && p.n_groups >= p.n_cand) a.peaks = reinterpret_cast<uint32_t*>(ws);
   if (p.pair) {
     a.floor = reinterpret_cast<uint32_t*>(ws + p.floor);
     if (cudaMemsetAsync(a.floor, 0, (size_t)R * 4, s) != cudaSuccess) return cuda_fail();
@@ -1720,6 +1722,7 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
   f.entropy = entropy;
   f.top_ids = top_ids;
   f.top_logprobs = top_logprobs;
+  f.peaks = a.peaks;
   int pairs = 0;
   if (p.pair) {
     if ((st = lp_pairs(dev, &pairs)) != VG_OK) return st;

@@ -541,7 +541,9 @@ vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* x, const vo
  * NaN logits make the row's log probabilities and entropy NaN and take no place
  * among the alternatives; where fewer than n_top logits are above -inf the rest
  * have id -1. R = 0 is a no-op. Two launches; workspace:
- * vg_token_logprobs_workspace_bytes(R, H, V, n_top) bytes, 16-byte aligned.
+ * vg_token_logprobs_workspace_bytes(R, H, V, n_top) bytes, 16-byte aligned,
+ * ZERO-FILLED before its first call; every call leaves what has to be zero so,
+ * for later calls (one at a time) of any shape, but not for other functions'.
  * Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED, VG_ERR_WORKSPACE, VG_ERR_CUDA.
  * ------------------------------------------------------------------------- */
 size_t vg_token_logprobs_workspace_bytes(int32_t R, int32_t H, int32_t V, int32_t n_top);

@@ -31,6 +31,7 @@ def call(h, lm, tokens, n_top, status=0):
     torch.cuda.synchronize()
     assert vgv.vg_get_device_status()[0] == status
     gd.check()
+    assert int(ws[:24 * 128 * 4].count_nonzero()) == 0  # what a later call relies on
     n = lambda t: None if t is None else t.cpu().numpy()
     return n(lp), n(en), n(ids), n(tl)
 
@@ -102,6 +103,35 @@ def test_many_rows_few_tokens(R, V, n_top):
 def test_full_vocabulary():
     h, lm, tok = inputs(8, DIMS.H, DIMS.V, seed=5, sure=14.0)
     check(h, lm, tok, 20)
+
+
+def test_one_workspace_for_calls_of_several_shapes():
+    """The words that have to be zero lie at one place in every cut, whatever ran
+    before: full rows, one token, several row blocks, a vocabulary of few tiles."""
+    shapes = [(128, 64, 9001, 20), (1, 64, 9001, 3), (300, 64, 2000, 8), (77, 64, 40, 20), (128, 64, 20000, 12), (128, 64, 9001, 20)]
+    ws = torch.zeros(max(vgv.vg_token_logprobs_workspace_bytes(*s) for s in shapes), dtype=torch.uint8, device="cuda")
+    for R, H, V, n_top in shapes:
+        h, lm, tok = inputs(R, H, V, seed=V, sure=6.0)
+        out = []
+        for w in (ws, torch.zeros_like(ws)):
+            t = [torch.zeros(R, device="cuda") for _ in "ab"] + [torch.zeros(R, n_top, dtype=d, device="cuda") for d in (torch.int32, torch.float32)]
+            vgv.vg_token_logprobs(dev(h), dev(lm), torch.from_numpy(tok).cuda(), *t, w)
+            out.append(t)
+        torch.cuda.synchronize()
+        assert vgv.vg_get_device_status()[0] == 0
+        assert all(torch.equal(x, y) for x, y in zip(*out)), (R, V)
+
+
+def test_alternatives_in_one_part_of_the_vocabulary():
+    """The best tokens all in one tile, and none elsewhere near them: the bound
+    from the other parts lets them all in."""
+    g = np.random.default_rng(21)
+    h, lm, tok = inputs(128, 64, 30000, seed=21)
+    big = oracle.widen(h).sum(0)
+    for at in (0, 17000, 29970):
+        l2 = lm.copy()
+        l2[at:at + 30] = oracle.round_bf16_bits(g.normal(0, 1, (30, 64)) + 3 * big / np.abs(big).max())
+        check(h, l2, tok, 20)
 
 
 def test_many_row_blocks():
