@@ -36,6 +36,9 @@ constexpr int kLpSpare = 4;
 constexpr int kLpM = 128;
 constexpr int kLpABytes = kLpM * kBK * 2;
 constexpr int kLpAux = 1024;
+constexpr int kLpPeaks = 24 * 768;       // words of LpArgs::peaks at most: 768 rows with lists of 24, 1,536 with 12
+// Its rows (as a constant: worked out, the NC addresses cost 40 registers and 1.3 us).
+__host__ __device__ constexpr int lp_peak_rows(bool pair, int nc) { return pair ? kLpPeaks / nc : kLpM; }
 constexpr int kLpChunk = 16;             // columns read from tensor memory at a time
 constexpr int kLpPend = 8 + kLpChunk;    // columns a row can have waiting for its candidate list
 
@@ -45,7 +48,7 @@ struct LpArgs {
   float* stat;                 // [n_groups][3][R]: m, S, T
   unsigned long long* cand;    // [n_groups][R][NC]: order-preserving keys, descending; 0 = none
   uint32_t* floor;             // [R] or null: order-preserving image of a logit that NC others reach (0: none known)
-  uint32_t* peaks;             // [NC][128] or null: images of the largest logits of NC parts of the vocabulary; zero between calls
+  uint32_t* peaks;             // [NC][lp_peak_rows] or null: images of the largest logits of NC parts of the vocabulary; zero between calls
 };
 
 // b_rows: vocabulary rows of a tile that one CTA holds
@@ -411,15 +414,15 @@ __global__ void __launch_bounds__(192, 1)
         };
         if (vb > g * a.group_tiles) {
           pass(true, true);
-        } else if (!PAIR && a.peaks) {
+        } else if (a.peaks && __any_sync(0xffffffffu, least == -INFINITY && r < a.R)) {
           // The first tile fixes what may enter the lists. NC parts of the
           // vocabulary, each the groups that leave one rest by NC, have a largest
           // logit each, so NC logits reach the smallest of those. Every CTA has its
           // first tile at about the same time: it gives its rows' maxima away, takes
           // the tile into the sums, and by then finds the others'. Of 129,280 tokens
           // some 400 reach the bound then, one or two of a CTA's 880; with what a
-          // CTA's own tile shows, 70 of them entered its list of 24 (128 rows, 20
-          // alternatives: 74 us where this takes 68; 4 rows 61.4 and 59.8).
+          // CTA's own tile shows, 70 of them entered its list of 24 (20 alternatives,
+          // 128 rows: 74 us where this takes 68; 256 rows 101 and 89).
           float top = -INFINITY;
 #pragma unroll 1
           for (int c0 = 0; c0 < cols; c0 += kLpChunk) {
@@ -431,14 +434,13 @@ __global__ void __launch_bounds__(192, 1)
               if (c0 + j < cols) top = fmaxf(top, __uint_as_float(zb[j]));
           }
           if (r < a.R && top > -INFINITY)
-            atomicMax(a.peaks + g % NC * kLpM + r, (uint32_t)(argmax_key(top, 0u) >> 32));
+            atomicMax(a.peaks + g % NC * lp_peak_rows(PAIR, NC) + r, (uint32_t)(argmax_key(top, 0u) >> 32));
           pass(true, false);
-          uint32_t f = 0u;
           if (r < a.R) {
-            f = 0xFFFFFFFFu;
+            uint32_t f = 0xFFFFFFFFu;
 #pragma unroll
-            for (int k = 0; k < NC; ++k) f = min(f, __ldcg(a.peaks + k * kLpM + r));
-            if (f > 0u) least = lp_below(lp_unkey(f));
+            for (int k = 0; k < NC; ++k) f = min(f, __ldcg(a.peaks + k * lp_peak_rows(PAIR, NC) + r));
+            if (f > 0u) least = fmaxf(least, lp_below(lp_unkey(f)));
           }
           if (__any_sync(0xffffffffu, least == -INFINITY && r < a.R)) own_bound();
           pass(false, true);
@@ -492,6 +494,7 @@ struct LpFinishArgs {
   int32_t* top_ids;       // [R, n_top]
   float* top_logprobs;    // [R, n_top]
   uint32_t* peaks;        // as in LpArgs
+  int peak_rows;
 };
 
 constexpr int kLpMaxGroups = 512;
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (a.peaks && tid < NC) a.peaks[tid * kLpM + r] = 0u;
+  if (a.peaks && tid < NC) a.peaks[tid * a.peak_rows + r] = 0u;
   const int tok = a.tokens ? a.tokens[r] : -1;
   if (tid == 0) n_pool = 0, floor_s = 1ull;  // 0 keys are no candidates
   if (tid < NC) best[tid] = 0ull, rank_s[tid] = 0;

@@ -1604,8 +1604,8 @@ namespace {
 
 // How a call is cut: vocabulary tile, tiles per unit of work, candidates per unit.
 struct LpPlan {
-  bool pair;
-  int tile_n, b_rows, stages, n_vblk, group_tiles, n_groups, n_mblk, n_cand;
+  bool pair, peaks;
+  int peak_rows, tile_n, b_rows, stages, n_vblk, group_tiles, n_groups, n_mblk, n_cand;
   size_t stat, cand, floor, total;
 };
 LpPlan lp_plan(int R, int V, int n_top) {
@@ -1646,7 +1646,10 @@ LpPlan lp_plan(int R, int V, int n_top) {
   p.stages = 8;
   while (lp_smem_bytes(p.b_rows, p.stages) > kMaxSmemBytes) --p.stages;
   // the words that have to be zero between calls lie first, in every plan
-  p.stat = align256((size_t)lp_cands(kLpMaxTop) * kLpM * 4);
+  p.peak_rows = lp_peak_rows(p.pair, p.n_cand);
+  // (the parts of the vocabulary that are at work at one time: pairs do n_rb row blocks side by side)
+  p.peaks = min(p.n_groups, workers / n_rb) >= p.n_cand && R <= p.peak_rows;
+  p.stat = kLpPeaks * 4;
   p.cand = p.stat + align256((size_t)p.n_groups * 3 * R * 4);
   p.floor = p.cand + align256((size_t)p.n_groups * R * p.n_cand * 8);
   p.total = p.floor + align256((size_t)R * 4);
@@ -1698,7 +1701,7 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
   a.stages = p.stages;
   a.stat = reinterpret_cast<float*>(ws + p.stat);
   a.cand = reinterpret_cast<unsigned long long*>(ws + p.cand);
-  if (!p.pair && p.n_groups >= p.n_cand) a.peaks = reinterpret_cast<uint32_t*>(ws);
+  a.peaks = p.peaks ? reinterpret_cast<uint32_t*>(ws) : nullptr;
   if (p.pair) {
     a.floor = reinterpret_cast<uint32_t*>(ws + p.floor);
     if (cudaMemsetAsync(a.floor, 0, (size_t)R * 4, s) != cudaSuccess) return cuda_fail();
@@ -1723,6 +1726,7 @@ extern "C" vg_status vg_token_logprobs(int32_t R, int32_t H, int32_t V, const vo
   f.top_ids = top_ids;
   f.top_logprobs = top_logprobs;
   f.peaks = a.peaks;
+  f.peak_rows = p.peak_rows;
   int pairs = 0;
   if (p.pair) {
     if ((st = lp_pairs(dev, &pairs)) != VG_OK) return st;

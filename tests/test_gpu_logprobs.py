@@ -31,7 +31,7 @@ def call(h, lm, tokens, n_top, status=0):
     torch.cuda.synchronize()
     assert vgv.vg_get_device_status()[0] == status
     gd.check()
-    assert int(ws[:24 * 128 * 4].count_nonzero()) == 0  # what a later call relies on
+    assert int(ws[:24 * 768 * 4].count_nonzero()) == 0  # what a later call relies on
     n = lambda t: None if t is None else t.cpu().numpy()
     return n(lp), n(en), n(ids), n(tl)
 
@@ -108,7 +108,7 @@ def test_full_vocabulary():
 def test_one_workspace_for_calls_of_several_shapes():
     """The words that have to be zero lie at one place in every cut, whatever ran
     before: full rows, one token, several row blocks, a vocabulary of few tiles."""
-    shapes = [(128, 64, 9001, 20), (1, 64, 9001, 3), (300, 64, 2000, 8), (77, 64, 40, 20), (128, 64, 20000, 12), (128, 64, 9001, 20)]
+    shapes = [(128, 64, 9001, 20), (1, 64, 9001, 3), (300, 64, 2000, 8), (77, 64, 40, 20), (128, 64, 20000, 12), (700, 64, 20000, 12), (1500, 64, 9001, 3), (128, 64, 9001, 20)]
     ws = torch.zeros(max(vgv.vg_token_logprobs_workspace_bytes(*s) for s in shapes), dtype=torch.uint8, device="cuda")
     for R, H, V, n_top in shapes:
         h, lm, tok = inputs(R, H, V, seed=V, sure=6.0)
@@ -122,11 +122,12 @@ def test_one_workspace_for_calls_of_several_shapes():
         assert all(torch.equal(x, y) for x, y in zip(*out)), (R, V)
 
 
-def test_alternatives_in_one_part_of_the_vocabulary():
+@pytest.mark.parametrize("R", [128, 300])
+def test_alternatives_in_one_part_of_the_vocabulary(R):
     """The best tokens all in one tile, and none elsewhere near them: the bound
     from the other parts lets them all in."""
     g = np.random.default_rng(21)
-    h, lm, tok = inputs(128, 64, 30000, seed=21)
+    h, lm, tok = inputs(R, 64, 30000, seed=21)
     big = oracle.widen(h).sum(0)
     for at in (0, 17000, 29970):
         l2 = lm.copy()
