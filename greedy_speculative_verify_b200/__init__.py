@@ -162,13 +162,19 @@ def _t():
     return _torch
 
 
+_raw_stream = _device = None
+
+
 def _stream(stream):
     if stream is None:
-        torch = _t()
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:  # the same handle, without the 3 us that a Stream object takes
-            return ctypes.c_void_p(raw(torch.cuda.current_device()))
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        global _raw_stream, _device
+        if _raw_stream is None:
+            torch = _t()
+            _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+            # the same handle, without the 3 us that a Stream object takes
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+            torch.cuda.current_device()  # (brings CUDA up, which the calls above do not)
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -384,9 +390,10 @@ def _same_device(device, *tensors):
     for t in tensors:
         if t is not None and t.device != device:
             raise ValueError(f"a tensor is on {t.device}, not on {device}")
-    if device.type != "cuda":
+    index = device.index
+    if index is None:  # host memory
         raise ValueError(f"tensors are on {device}, not on a CUDA device")
-    if device.index != _t().cuda.current_device():
+    if index != (_device or _t().cuda.current_device)():
         raise ValueError(f"tensors are on {device}, which is not the current device")
 
 
