@@ -608,7 +608,8 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   }
   __syncthreads();
   // ---- their logits from exact products (a product of two bf16 is exact in fp32),
-  // summed in fp64; a warp takes two candidates at a time
+  // summed in fp64; a warp takes two candidates at a time (the conversions to fp64,
+  // 16 a clock, are the cost: none for a second candidate that is not there)
   for (int k0 = warp; k0 <= NC; k0 += 2 * NW) {
     int v[2];
     double z[2] = {0.0, 0.0};
@@ -624,19 +625,24 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
       const uint4* w0 = reinterpret_cast<const uint4*>(a.lm + (size_t)(v[0] >= 0 ? v[0] : v[1]) * a.H);
       const uint4* w1 = reinterpret_cast<const uint4*>(a.lm + (size_t)(v[1] >= 0 ? v[1] : v[0]) * a.H);
       double y[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
-#pragma unroll 5
-      for (int i = lane; i < a.H / 8; i += 32) {
-        const uint4 xv = x[i], wv[2] = {w0[i], w1[i]};
-        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
+      auto add = [&](int c, const uint4& xv, const uint4& wv) {
+        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w}, ws[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t ws[4] = {wv[c].x, wv[c].y, wv[c].z, wv[c].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[c][0] += (double)(bf16_lo(xs[e]) * bf16_lo(ws[e]));
-            y[c][1] += (double)(bf16_hi(xs[e]) * bf16_hi(ws[e]));
-          }
+        for (int e = 0; e < 4; ++e) {
+          y[c][0] += (double)(bf16_lo(xs[e]) * bf16_lo(ws[e]));
+          y[c][1] += (double)(bf16_hi(xs[e]) * bf16_hi(ws[e]));
         }
+      };
+      if (v[1] >= 0) {
+#pragma unroll 5
+        for (int i = lane; i < a.H / 8; i += 32) {
+          const uint4 xv = x[i], wv[2] = {w0[i], w1[i]};
+          add(0, xv, wv[0]);
+          add(1, xv, wv[1]);
+        }
+      } else {
+#pragma unroll 5
+        for (int i = lane; i < a.H / 8; i += 32) add(0, x[i], w0[i]);
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) z[c] = y[c][0] + y[c][1];
