@@ -45,7 +45,7 @@ constexpr int kLpPend = 8 + kLpChunk;    // columns a row can have waiting for i
 struct LpArgs {
   int R, V, k_chunks, n_mblk, n_vblk, group_tiles, n_groups, a_box_rows, b_box_rows;
   int tile_n, stages;          // vocabulary rows per tile, pipeline stages
-  float* stat;                 // [n_groups][3][R]: m, S, T
+  float* stat;                 // [n_groups][4][R]: m, S, T, what rounding took off S
   unsigned long long* cand;    // [n_groups][R][NC]: order-preserving keys, descending; 0 = none
   uint32_t* floor;             // [R] or null: order-preserving image of a logit that NC others reach (0: none known)
   uint32_t* peaks;             // [NC][lp_peak_rows] or null: images of the largest logits of NC parts of the vocabulary; zero between calls
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(192, 1)
       const int vb1 = min(a.n_vblk, (g + 1) * a.group_tiles);
       const int r = mb * kLpM + row;
       const bool busy = mb * kLpM + q * 32 < a.R;  // this warp has rows
-      float m = -INFINITY, S = 0.0f, T = 0.0f;
+      float m = -INFINITY, S = 0.0f, T = 0.0f, low = 0.0f;
       float least = -INFINITY;  // only larger logits enter
       int parked = 0;
       list.clear();
@@ -388,17 +388,26 @@ __global__ void __launch_bounds__(192, 1)
               if (now > m && m > -INFINITY) {  // to the new maximum
                 const float d = fmaxf(m - now, -1000.0f), f = ex2(d * 1.4426950408889634f);
                 T = f * (T + S * d);
-                S *= f;
+                S *= f, low *= f;
               }
               m = now;
-              float s1 = 0.0f, t1 = 0.0f;
+              float e[kLpChunk], t1 = 0.0f;
 #pragma unroll
               for (int j = 0; j < kLpChunk; ++j) {
-                const float d = z[j] - base, e = ex2(d * 1.4426950408889634f);
-                s1 += e;
-                t1 = fmaf(e, fmaxf(d, -1000.0f), t1);  // a weight of 0 adds 0, also where z is -inf
+                const float d = z[j] - base;
+                e[j] = ex2(d * 1.4426950408889634f);
+                t1 = fmaf(e[j], fmaxf(d, -1000.0f), t1);  // a weight of 0 adds 0, also where z is -inf
               }
-              S += s1;
+              // Where one token has nearly all the mass its log probability is what
+              // the others add to its 1: summed in pairs, so that the 1 is rounded
+              // with four times a chunk, and with the rounding of S kept.
+#pragma unroll
+              for (int n = kLpChunk / 2; n > 0; n /= 2)
+#pragma unroll
+                for (int j = 0; j < n; ++j) e[j] += e[j + n];
+              const float sum = S + e[0], back = sum - S;
+              low += (S - (sum - back)) + (e[0] - back);
+              S = sum;
               T += t1;
             }
             if (lists && __any_sync(0xffffffffu, top > least)) {
@@ -459,10 +468,11 @@ __global__ void __launch_bounds__(192, 1)
       }
       if (busy) settle();
       if (ok && r < a.R) {
-        float* st = a.stat + (size_t)g * 3 * a.R + r;
+        float* st = a.stat + (size_t)g * 4 * a.R + r;
         st[0] = m;
         st[a.R] = S;
         st[2 * (size_t)a.R] = T;
+        st[3 * (size_t)a.R] = low;
         unsigned long long* dst = a.cand + ((size_t)g * a.R + r) * NC;
 #pragma unroll
         for (int k = 0; k < NC; ++k) dst[k] = list.v[k] >= 0 ? argmax_key(list.z[k], (uint32_t)list.v[k]) : 0ull;
@@ -516,7 +526,7 @@ template <int NC, int NT>
 __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   constexpr int NW = NT / 32, kOwn = kLpMaxGroups / NT;  // units a thread may own: tid, tid + NT, ..
   __shared__ float red_m[NW];
-  __shared__ double red_s[NW], red_t[NW], z_s[NC + 1], s_fix[kLpFix], t_fix[kLpFix];
+  __shared__ double red_s[NW], red_t[NW], z_s[NC + 1], s_fix[kLpFix], t_fix[kLpFix], s_raw[kLpFix], t_raw[kLpFix], short_of[kLpFix], square[kLpFix];
   __shared__ unsigned long long head[kLpMaxGroups], pool[NC * NC], best[NC];
   __shared__ unsigned long long floor_s;
   __shared__ int id_s[NC + 1], rank_s[NC], head_rank[kLpMaxGroups], n_pool;
@@ -529,15 +539,15 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   if (tid < NC) best[tid] = 0ull, rank_s[tid] = 0;
   for (int g = tid; g < a.n_groups; g += NT) head_rank[g] = 0;
   // ---- the units' sums, rescaled to the common maximum
-  float mg[kOwn], Sg[kOwn], Tg[kOwn], m = -INFINITY;
+  float mg[kOwn], Sg[kOwn], Tg[kOwn], low[kOwn], m = -INFINITY;
   unsigned long long first[kOwn];
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
     const int g = tid + i * NT;
-    mg[i] = -INFINITY, Sg[i] = Tg[i] = 0.0f, first[i] = 0ull;
+    mg[i] = -INFINITY, Sg[i] = Tg[i] = low[i] = 0.0f, first[i] = 0ull;
     if (g < a.n_groups) {
-      const float* st = a.stat + (size_t)g * 3 * a.R + r;
-      mg[i] = st[0], Sg[i] = st[a.R], Tg[i] = st[2 * (size_t)a.R];
+      const float* st = a.stat + (size_t)g * 4 * a.R + r;
+      mg[i] = st[0], Sg[i] = st[a.R], Tg[i] = st[2 * (size_t)a.R], low[i] = st[3 * (size_t)a.R];
       first[i] = a.cand[((size_t)g * a.R + r) * NC];
       head[g] = first[i];
     }
@@ -568,7 +578,7 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
       if (i * NT >= a.n_groups) break;
       // a unit's largest term is 1 before rescaling, so the factor needs fp32 accuracy only
       const float d = mg[i] > -INFINITY ? mg[i] - m : 0.0f, f = mg[i] > -INFINITY ? ex2(d * 1.4426950408889634f) : 1.0f;
-      S += (double)f * Sg[i];
+      S += (double)f * ((double)Sg[i] + (double)low[i]);
       T += (double)f * ((double)Tg[i] + (double)Sg[i] * fmaxf(d, -1000.0f));
     }
 #pragma unroll
@@ -661,15 +671,16 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   if (tid == 0 && tok >= a.V) record_error(kErrBounds, 355);
   __syncthreads();
   if (tid < kLpFix) {  // what the exact logits change in S and T
-    double ds = 0.0, dt = 0.0;
+    double ds = 0.0, dt = 0.0, s0 = 0.0, t0 = 0.0, off = 0.0, sq = 0.0;
     if (id_s[tid] >= 0 && m < INFINITY) {
-      const double d0 = (double)lp_unkey((uint32_t)(best[tid] >> 32)) - (double)m, d1 = z_s[tid] - (double)m;
+      const double z0 = (double)lp_unkey((uint32_t)(best[tid] >> 32)), d0 = z0 - (double)m, d1 = z_s[tid] - (double)m;
       // e^d1 - e^d0 = e^d0 (e^(d1 - d0) - 1): d1 - d0 is a rounding's worth, and needs no more than fp32 accuracy
       const double e0 = (double)expf((float)d0), g = d1 - d0, gain = (double)expm1f((float)g);
       ds = e0 * gain;
       dt = e0 * (g + gain * d1);
+      s0 = e0, t0 = e0 * d0, off = g * z0, sq = z0 * z0;
     }
-    s_fix[tid] = ds, t_fix[tid] = dt;
+    s_fix[tid] = ds, t_fix[tid] = dt, s_raw[tid] = s0, t_raw[tid] = t0, short_of[tid] = off, square[tid] = sq;
   }
   // ---- order: rank of each candidate by (logit, lower index first); those that are
   // missing (fewer logits above -inf than asked for) come last, in list order
@@ -680,13 +691,27 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   }
   __syncthreads();
   if (warp != 0) return;
-  S = T = 0.0;
-  if (lane < NW && lane * 32 < a.n_groups) S = red_s[lane], T = red_t[lane];
-  if (lane < kLpFix) S += s_fix[lane], T += t_fix[lane];
+  // The other tokens' logits fell short like these, by a share of themselves (the
+  // least squares' over the candidates; no more than half a place for each 16
+  // products): their mean logit's worth is put back on their S and T.
+  double sum[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};  // S, T, then of the candidates: S, T, shortfall times logit, logit squared
+  if (lane < NW && lane * 32 < a.n_groups) sum[0] = red_s[lane], sum[1] = red_t[lane];
+  if (lane < kLpFix) sum[2] = s_raw[lane], sum[3] = t_raw[lane], sum[4] = short_of[lane], sum[5] = square[lane];
+  double ds = lane < kLpFix ? s_fix[lane] : 0.0, dt = lane < kLpFix ? t_fix[lane] : 0.0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    S += __shfl_xor_sync(0xffffffffu, S, o);
-    T += __shfl_xor_sync(0xffffffffu, T, o);
+    ds += __shfl_xor_sync(0xffffffffu, ds, o);
+    dt += __shfl_xor_sync(0xffffffffu, dt, o);
+#pragma unroll
+    for (int k = 0; k < 6; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+  }
+  S = sum[0] + ds, T = sum[1] + dt;
+  const double rest = sum[0] - sum[2], rest_t = sum[1] - sum[3];
+  if (sum[5] > 0.0 && rest > 0.0 && rest < INFINITY) {
+    const double share = fmin(fmax(sum[4] / sum[5], 0.0), (double)(a.H / 16) * 5.9604645e-8);
+    const double move = share * ((double)m + rest_t / rest);
+    S += move * rest;
+    T += move * (rest + rest_t);
   }
   const double log_s = log(S), lse = (double)m + log_s;
   if (lane == 0) {

@@ -1650,7 +1650,7 @@ LpPlan lp_plan(int R, int V, int n_top) {
   // (the parts of the vocabulary that are at work at one time: pairs do n_rb row blocks side by side)
   p.peaks = min(p.n_groups, workers / n_rb) >= p.n_cand && R <= p.peak_rows;
   p.stat = kLpPeaks * 4;
-  p.cand = p.stat + align256((size_t)p.n_groups * 3 * R * 4);
+  p.cand = p.stat + align256((size_t)p.n_groups * 4 * R * 4);
   p.floor = p.cand + align256((size_t)p.n_groups * R * p.n_cand * 8);
   p.total = p.floor + align256((size_t)R * 4);
   return p;

@@ -527,7 +527,8 @@ vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* x, const vo
  *   top_ids[r, 0 .. n_top-1]      = the n_top largest z[r,v], equal ones by lower v
  *   top_logprobs[r, j]            = z[r, top_ids[r,j]] - lse[r]
  * The logits are never stored. lse and the entropy come from tensor-core logits
- * (fp32 sums); the given tokens' and the alternatives' logits are recomputed as
+ * (fp32 sums, which fall short by up to 1e-8 of a logit for 16 products: that is
+ * put back by what the largest logits fell short of their exact values); the given tokens' and the alternatives' logits are recomputed as
  * exact products summed in fp64, so the order of close alternatives is that of
  * the exact logits (an alternative can be missed only if more than four others
  * lie within fp32 rounding of the n_top-th).

@@ -100,6 +100,29 @@ def test_many_rows_few_tokens(R, V, n_top):
     check(h, lm, tok, n_top)
 
 
+@pytest.mark.parametrize("R,V", [(3, 9000), (260, 9000)])
+def test_tokens_with_nearly_all_the_mass(R, V):
+    """Their log probability is what the others add to a sum of 1. The 1 is rounded
+    with at most four times inside a chunk of 16 logits and once more into the sum,
+    which keeps that rounding, and once where S is rescaled: 6 times 2^-24. What the
+    others add is off as in tolerances(), in proportion to their mass."""
+    H = 64
+    g = np.random.default_rng(31)
+    lm = g.normal(0, 1.2 / np.sqrt(H), (V, H))
+    tok = g.choice(V, R, replace=False).astype(np.int32)
+    lm[tok] *= 2.5
+    lm = oracle.round_bf16_bits(lm)
+    w = oracle.widen(lm)[tok]
+    h = oracle.round_bf16_bits(g.uniform(14, 19, (R, 1)) * w / (w * w).sum(1, keepdims=True))
+    lp, ent, mag = kv8.logprobs(h, lm)
+    want = lp[np.arange(R), tok]
+    assert (want > -0.2).mean() > 0.9  # the test's point: rows of the kind it is about
+    got, _, _, _ = call(dev(h), dev(lm), torch.from_numpy(tok).cuda(), 5)
+    ez = 6 * np.sqrt(H) * 2.0 ** -23 * mag.max(axis=1)
+    tol = 6 * 2.0 ** -24 + (ez + 128 * 2.0 ** -24 + 2.0 ** -21) * (1 - np.exp(want)) + 2.0 ** -24 * np.abs(want)
+    assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / tol).max())
+
+
 def test_full_vocabulary():
     h, lm, tok = inputs(8, DIMS.H, DIMS.V, seed=5, sure=14.0)
     check(h, lm, tok, 20)
