@@ -227,7 +227,10 @@ __global__ void __launch_bounds__(192, 1)
       for (int s = 0; s < stages; ++s)
         if (rank == 0 && (issued & (1u << s))) mbar_wait(&full[s], (last_par >> s) & 1, limit);
     }
-  } else if (warp == 1 && PAIR && rank == 1) {  // the even CTA issues the pair's MMAs
+  } else if (warp == 1 && PAIR && rank == 1) {
+    // The even CTA issues the pair's MMAs; its commits arrive on this CTA's barriers
+    // too, the last of them on mma_done: not to leave before that has come.
+    if (lane == 0) mbar_wait(mma_done, 0, limit);
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16_f32(PAIR ? 2 * kLpM : kLpM, a.tile_n);

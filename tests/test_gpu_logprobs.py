@@ -310,3 +310,24 @@ def test_verify_step_with_logprobs():
         assert torch.equal(ids[committed, 0], tok.view(-1)[committed])
         assert torch.equal(lp[committed], tl[committed, 0])
         assert bool((lp[~committed] == -torch.inf).all()) and bool((tl[:, 0] >= tl[:, 1]).all()) and bool((en > 0).all())
+
+
+def test_pairs_of_ctas_call_after_call():
+    """Several row blocks over vocabularies of one to a few tiles, one call right
+    behind the other: pairs whose even CTA has work left to signal when the odd
+    one has stored its rows. Every call gives the first one's bits."""
+    runs = []
+    for R, V, n_top in ((129, 40, 3), (300, 256, 20), (257, 700, 8)):
+        h, lm, tok = inputs(R, 64, V, seed=R, sure=4.0)
+        t = [torch.zeros(R, device="cuda") for _ in "ab"] + [torch.zeros(R, n_top, dtype=d, device="cuda") for d in (torch.int32, torch.float32)]
+        ws = torch.zeros(vgv.vg_token_logprobs_workspace_bytes(R, 64, V, n_top), dtype=torch.uint8, device="cuda")
+        runs.append((dev(h), dev(lm), torch.from_numpy(tok).cuda(), t, ws))
+    first = None
+    for _ in range(50):
+        for h, lm, tok, t, ws in runs:
+            vgv.vg_token_logprobs(h, lm, tok, *t, ws)
+        torch.cuda.synchronize()
+        assert vgv.vg_get_device_status()[0] == 0
+        got = [x.clone() for r in runs for x in r[3]]
+        first = first or got
+        assert all(torch.equal(x, y) for x, y in zip(first, got))
