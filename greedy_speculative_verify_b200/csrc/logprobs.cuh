@@ -696,7 +696,12 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   if (warp != 0) return;
   // The other tokens' logits fell short like these, by a share of themselves (the
   // least squares' over the candidates; no more than half a place for each 16
-  // products): their mean logit's worth is put back on their S and T.
+  // products): their mean logit's worth is put back on their S and T. What is left of
+  // the sums without the candidates is a difference: where these hold all the mass it
+  // is rounding alone, a residue of 1e-16 beside one of 1e-8 in T, and their quotient
+  // any number. So both are kept within what the other tokens can be: V - kLpFix of
+  // them, none above the last candidate, and none below where ex2 gives 0. (Two tokens
+  // with all the mass, H = 8,192: the entropy was off by up to 1e-4 without.)
   double sum[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};  // S, T, then of the candidates: S, T, shortfall times logit, logit squared
   if (lane < NW && lane * 32 < a.n_groups) sum[0] = red_s[lane], sum[1] = red_t[lane];
   if (lane < kLpFix) sum[2] = s_raw[lane], sum[3] = t_raw[lane], sum[4] = short_of[lane], sum[5] = square[lane];
@@ -709,12 +714,15 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
     for (int k = 0; k < 6; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
   }
   S = sum[0] + ds, T = sum[1] + dt;
-  const double rest = sum[0] - sum[2], rest_t = sum[1] - sum[3];
-  if (sum[5] > 0.0 && rest > 0.0 && rest < INFINITY) {
+  const unsigned long long last = best[kLpFix - 1];  // (0: there are no others)
+  const double most = last ? (double)lp_unkey((uint32_t)(last >> 32)) - (double)m : -INFINITY;
+  const double rest = fmin(sum[0] - sum[2], 1.0001 * (double)(a.V - kLpFix) * (double)expf((float)most));
+  if (sum[5] > 0.0 && rest > 0.0) {
     const double share = fmin(fmax(sum[4] / sum[5], 0.0), (double)(a.H / 16) * 5.9604645e-8);
-    const double move = share * ((double)m + rest_t / rest);
-    S += move * rest;
-    T += move * (rest + rest_t);
+    const double mean = fmin(fmax((sum[1] - sum[3]) / rest, -88.0), most);
+    const double move = share * ((double)m + mean) * rest;
+    S += move;
+    T += move * (1.0 + mean);
   }
   const double log_s = log(S), lse = (double)m + log_s;
   if (lane == 0) {

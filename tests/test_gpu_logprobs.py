@@ -331,3 +331,46 @@ def test_pairs_of_ctas_call_after_call():
         got = [x.clone() for r in runs for x in r[3]]
         first = first or got
         assert all(torch.equal(x, y) for x, y in zip(first, got))
+
+
+def test_two_tokens_with_all_the_mass():
+    """Nothing is left of the sums beside the candidates, down to one unit in the
+    last place of fp64, and no quotient of such rest enters the entropy. Rows along
+    one direction, tokens at multiples of it: two near the top, 16 a factor of 1e-15
+    below, the others far off, at H = 8192, where the tensor cores fall short most.
+    The candidates' logits are exact, so what is off is the exponential's argument
+    d log2(e) (two roundings: |d| 2^-23), the exponential (2^-22), and in S and T at
+    most three roundings of 2^-24 each for the two tokens that count, weighted with
+    p (1 + |d|); the result's rounding comes on top."""
+    H, V, R = 8192, 32, 128
+    for seed, tail in ((1, -15.5), (2, -16.5), (3, -17.5)):
+        g = np.random.default_rng(seed)
+        a = np.full(V, -80.0)
+        a[:2], a[16:] = (20.0, 19.0), tail + g.uniform(-0.3, 0.3, 16)
+        u = g.normal(0, 1, H)
+        lm = oracle.round_bf16_bits(a[:, None] * u / np.sqrt(H))
+        h = oracle.round_bf16_bits(g.uniform(0.9, 1.1, (R, 1)) * u / np.sqrt((u * u).mean()) / np.sqrt(H))
+        lp, ent, _ = kv8.logprobs(h, lm)
+        assert (np.sort(lp, 1)[:, -3] < -30).all() and (ent > 0.4).all()
+        lpt, en, _, _ = call(dev(h), dev(lm), torch.zeros(R, dtype=torch.int32).cuda(), 5)
+        p, d = np.exp(lp), np.abs(lp - lp.max(1, keepdims=True))
+        tol = (p * (1 + d) * (2.0 ** -22 + d * 2.0 ** -23 + 3 * 2.0 ** -24)).sum(1)
+        assert (np.abs(en - ent) <= tol + 2.0 ** -24 * ent).all(), float((np.abs(en - ent) / tol).max())
+        assert (np.abs(lpt - lp[:, 0]) <= tol + 2.0 ** -24 * np.abs(lp[:, 0])).all()
+
+
+@pytest.mark.parametrize("V,H", [(2, 8192), (3, 1280), (7, 8192), (12, 1280), (12, 8192), (13, 8192)])
+def test_hardly_more_tokens_than_candidates(V, H):
+    """All tokens, or all but one, are among the candidates with exact logits: what
+    is off is as in the test above, with the roundings of V terms (a chain of them in
+    T, of 16 at most; log2 of 16 and one more in S)."""
+    h, lm, tok = inputs(64, H, V, seed=V + H, sure=4.0)
+    lp, ent, mag = kv8.logprobs(h, lm)
+    got, en, _, _ = call(dev(h), dev(lm), torch.from_numpy(tok).cuda(), 2 if V < 5 else 5)
+    p, d = np.exp(lp), np.abs(lp - lp.max(1, keepdims=True))
+    tol = (p * (1 + d) * (2.0 ** -22 + d * 2.0 ** -23 + min(V, 16) * 2.0 ** -24)).sum(1)
+    if V > 12:  # the last token's logit stays the tensor cores'
+        tol = tol + (np.sort(p, 1)[:, 0] * (1 + d.max(1)) * 2) * 6 * np.sqrt(H) * 2.0 ** -23 * mag.max(1)
+    want = lp[np.arange(64), tok]
+    assert (np.abs(en - ent) <= tol + 2.0 ** -24 * ent).all(), float((np.abs(en - ent) / tol).max())
+    assert (np.abs(got - want) <= tol + 2.0 ** -24 * np.abs(want)).all()
