@@ -341,13 +341,14 @@ struct Kv8Warp {
     }
   }
 
-  // real: how many of the group's positions are the sequence's
+  // lo, hi: the sequence's positions that any row sees, counted from the group's first
   __device__ __forceinline__ void values(const uint4 (&vf)[DIM / 32], const uint32_t (&b0)[NT], const uint32_t (&b1)[NT],
-                                         int real, int lane) {
+                                         int lo, int hi, int lane) {
     uint32_t keep = 0xFFFFFFFFu;
-    if (FMT == kKv8E4m3 && real < kKv8Group) {  // a code never written may be NaN, and 0 * NaN is not 0
-      const int mine = real - 4 * (lane & 3);
-      keep = mine >= 4 ? 0xFFFFFFFFu : mine <= 0 ? 0u : (1u << (8 * mine)) - 1u;
+    if (FMT == kKv8E4m3 && (lo > 0 || hi < kKv8Group)) {  // a code never written may be NaN, and 0 * NaN is not 0
+      const int p = 4 * (lane & 3);
+      if (hi < p + 4) keep = hi <= p ? 0u : 0xFFFFFFFFu >> (8 * (p + 4 - hi));
+      if (lo > p) keep = lo >= p + 4 ? 0u : keep & (0xFFFFFFFFu << (8 * (lo - p)));
     }
 #pragma unroll
     for (int j = 0; j < DIM / 32; ++j) {
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(32 * kKaWarps, ka_ctas(NT)) kv8_attn(const Kv8
       w.weights(z, ks_now, vs_now, p0, s.lo, p0 >= s.lo && p0 + kKv8Group - 1 <= s.L, lane, b0, b1);
       ka_cp_wait<2 * S - 1>();
       ka_lds(vf, ring + slot * kSlot + kHalf);
-      w.values(vf, b0, b1, s.hi - p0, lane);
+      w.values(vf, b0, b1, s.lo - p0, s.hi - p0, lane);
       if (more) load_v(slot);
       ka_cp_commit();
       if (++slot == S) slot = 0;

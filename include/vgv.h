@@ -457,6 +457,9 @@ typedef struct vg_kv8 {
  * round(x * Q / a). Every rounding is to nearest, ties to even, of the exact
  * quotient. So a decode step that rewrites the positions of rejected drafts
  * leaves a block's magnitude at least as large as those drafts needed.
+ * The stored magnitude counts wherever pos[b] is not a multiple of block, even
+ * if no earlier position of that block was ever written (a sequence whose first
+ * position lies inside a block): it has to be initialised then, to 0.
  * A NaN is stored as 0 and an infinity as the largest code of its sign, neither
  * counts for the magnitude, and VG_ERR_DEVICE_BOUNDS is recorded. pos[b] < 0,
  * n_new[b] outside [0, rows] or pos[b] + n_new[b] > L_max records

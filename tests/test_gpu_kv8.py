@@ -313,6 +313,23 @@ def test_attention_never_reads_unwritten_positions(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,group,never", [(128, 1, 0x7F), (128, 4, 0xFF), (64, 4, 0x7F), (64, 1, 0xFF)])
+def test_attention_never_reads_positions_before_the_first(fmt, dim, group, never):
+    """Sequences that start inside a group of 16 (padded on the left): the bytes
+    before their first position were never written either, and are NaN in e4m3."""
+    pos, rows, more = [0, 1, 3, 5, 15, 17, 30, 100, 131, 200], 3, 90
+    c = Cache(fmt, len(pos), 2, 320, dim, 64, seed=23, fill=False, never=never)
+    for y in "kv":  # magnitudes that the rows do not outgrow: earlier codes stay as they are
+        c.amax[y][:] = 8.0
+        c.t[y + "a"].fill_(8.0)
+    n = [1 + rows if b % 2 else more + rows for b in range(len(pos))]
+    c.append(more + rows, pos, n)
+    ok()
+    assert all((c.t[y].view(torch.uint8) == never).any() for y in "kv")
+    check_attention(c, rows, 2 * group, [p + m - rows for p, m in zip(pos, n)], first=pos)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_attention_extreme_scores(fmt):
     """Scores of several hundred (one position takes all), and queries and
     magnitudes near both ends of the bf16 range."""
