@@ -446,7 +446,6 @@ def make_kv8(k, v, k_amax, v_amax):
                k_amax.data_ptr(), v_amax.data_ptr())
     c.tensors = (k, v, k_amax, v_amax)
     c.device = k.device
-    c.ref = ctypes.byref(c)
     return c
 
 
@@ -459,7 +458,7 @@ def vg_kv8_append(cache, rows, k, v, pos, n_new=None, stream=None):
     _dense("pos", pos, (B,), torch.int32)
     _dense("n_new", n_new, (B,), torch.int32)
     _same_device(cache.device, k, v, pos, n_new)
-    _check(load().vg_kv8_append(cache.ref, rows, _at(k), ks, _at(v), vs, _at(pos), _at(n_new), _stream(stream)),
+    _check(load().vg_kv8_append(cache, rows, _at(k), ks, _at(v), vs, _at(pos), _at(n_new), _stream(stream)),
            "vg_kv8_append")
 
 
@@ -476,12 +475,12 @@ def vg_kv8_read(cache, rows, pos, k_out, v_out, n_rows=None, stream=None):
     _dense("n_rows", n_rows, (B,), torch.int32)
     _same_device(cache.device, k_out, v_out, pos, n_rows)
     kind = VG_F32 if out is not None and out.dtype is torch.float32 else VG_BF16
-    _check(load().vg_kv8_read(cache.ref, rows, _at(pos), _at(n_rows), kind, _at(k_out), ks, _at(v_out), vs,
+    _check(load().vg_kv8_read(cache, rows, _at(pos), _at(n_rows), kind, _at(k_out), ks, _at(v_out), vs,
                               _stream(stream)), "vg_kv8_read")
 
 
 def vg_kv8_attn_workspace_bytes(cache, rows, n_heads):
-    return load().vg_kv8_attn_workspace_bytes(cache.ref, rows, n_heads)
+    return load().vg_kv8_attn_workspace_bytes(cache, rows, n_heads)
 
 
 def vg_kv8_attn(cache, rows, n_heads, q, lens, scale, o, workspace, first=None, n_new=None, stream=None):
@@ -494,12 +493,12 @@ def vg_kv8_attn(cache, rows, n_heads, q, lens, scale, o, workspace, first=None, 
     _dense("first", first, (B,), torch.int32)
     _dense("n_new", n_new, (B,), torch.int32)
     _same_device(cache.device, q, o, lens, first, n_new, workspace)
-    _check(load().vg_kv8_attn(cache.ref, rows, n_heads, _at(q), qs, _at(lens), _at(first), _at(n_new), scale, _at(o), os_,
+    _check(load().vg_kv8_attn(cache, rows, n_heads, _at(q), qs, _at(lens), _at(first), _at(n_new), scale, _at(o), os_,
                               _at(workspace), _bytes_of(workspace), _stream(stream)), "vg_kv8_attn")
 
 
 def vg_attn_verify_kv8_workspace_bytes(cache, K):
-    return load().vg_attn_verify_kv8_workspace_bytes(cache.ref, K)
+    return load().vg_attn_verify_kv8_workspace_bytes(cache, K)
 
 
 def vg_attn_verify_kv8(cache, K, x, w_qkv, w_o, lens, out, workspace, o_out=None, stream=None):
@@ -512,7 +511,7 @@ def vg_attn_verify_kv8(cache, K, x, w_qkv, w_o, lens, out, workspace, o_out=None
         _dense(name, t, shape, bf16)
     _dense("lens", lens, (cache.B,), torch.int32)
     _same_device(cache.device, x, w_qkv, w_o, lens, out, o_out, workspace)
-    _check(load().vg_attn_verify_kv8(cache.ref, K, _at(x), _at(w_qkv), _at(w_o), _at(lens), _at(out), _at(o_out),
+    _check(load().vg_attn_verify_kv8(cache, K, _at(x), _at(w_qkv), _at(w_o), _at(lens), _at(out), _at(o_out),
                                      _at(workspace), _bytes_of(workspace), _stream(stream)), "vg_attn_verify_kv8")
 
 

@@ -1,6 +1,8 @@
 """Refusals of the 8-bit cache and log-probability calls, before any CUDA call
 (CPU only)."""
 import ctypes
+import gc
+import weakref
 
 import pytest
 import torch
@@ -152,3 +154,21 @@ def test_binding_refuses_host_tensors():
                  lambda: vgv.vg_token_logprobs(h, h.clone(), i, f, None, None, None, ws)):
         with pytest.raises(ValueError, match="not on a CUDA device"):
             call()
+
+
+def test_handle_lets_its_tensors_go():
+    """Without its handle and the caller's names a cache's memory is free at once,
+    not when a collector next runs; a call with the handle changes nothing in that."""
+    k, a = torch.zeros(2, 3, 64, 64, dtype=torch.int8), torch.zeros(2, 3, 4)
+    v, b = k.clone(), a.clone()
+    c = vgv.make_kv8(k, v, a, b)
+    assert vgv.vg_kv8_attn_workspace_bytes(c, 4, 3) > 0 and c.k == k.data_ptr()
+    held = [weakref.ref(t) for t in (k, v, a, b)]
+    gc.disable()
+    try:
+        del k, v, a, b
+        assert all(r() is not None for r in held)  # the handle keeps them
+        del c
+        assert all(r() is None for r in held)
+    finally:
+        gc.enable()
