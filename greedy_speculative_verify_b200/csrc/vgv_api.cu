@@ -1303,6 +1303,14 @@ bool kv8_overlaps(const vg_kv8* c, const void* p, size_t bytes) {
                           overlaps(c->k_amax, am, p, bytes) || overlaps(c->v_amax, am, p, bytes));
 }
 
+// Whether two of the cache's four parts share memory: a call that writes them
+// would write one over the other.
+bool kv8_parts_collide(const vg_kv8* c) {
+  const size_t codes = kv8_code_bytes(c), am = (size_t)c->B * c->n_kv * (c->L_max / c->block) * 4;
+  return overlaps(c->k, codes, c->v, codes) || overlaps(c->k_amax, am, c->v_amax, am) || overlaps(c->k, codes, c->k_amax, am) ||
+         overlaps(c->k, codes, c->v_amax, am) || overlaps(c->v, codes, c->k_amax, am) || overlaps(c->v, codes, c->v_amax, am);
+}
+
 vg::Kv8View kv8_view(const vg_kv8* c) {
   int log2 = 4;
   while ((1 << log2) < c->block) ++log2;
@@ -1441,7 +1449,8 @@ extern "C" vg_status vg_kv8_append(const vg_kv8* c, int32_t rows, const void* k,
       v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride > (1 << 24) || v_stride > (1 << 24))
     return VG_ERR_INVALID_ARG;
   if ((int64_t)c->B * c->n_kv * ((rows + c->block - 2) / c->block + 1) * 2 >= ((int64_t)1 << 31)) return VG_ERR_UNSUPPORTED;
-  if (kv8_overlaps(c, k, rows_span(R, k_stride, width, 2)) || kv8_overlaps(c, v, rows_span(R, v_stride, width, 2)))
+  if (kv8_parts_collide(c) || kv8_overlaps(c, k, rows_span(R, k_stride, width, 2)) ||
+      kv8_overlaps(c, v, rows_span(R, v_stride, width, 2)))
     return VG_ERR_INVALID_ARG;
   DevState* dev = nullptr;
   if ((st = device_state(&dev)) != VG_OK) return st;
@@ -1564,7 +1573,7 @@ extern "C" vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* 
     return VG_ERR_INVALID_ARG;
   const int R = c->B * (K + 1);
   const size_t rows_bytes = (size_t)R * kH * 2;
-  if (overlaps(x, rows_bytes, out, rows_bytes) || kv8_overlaps(c, out, rows_bytes)) return VG_ERR_INVALID_ARG;
+  if (overlaps(x, rows_bytes, out, rows_bytes) || kv8_overlaps(c, out, rows_bytes) || kv8_parts_collide(c)) return VG_ERR_INVALID_ARG;
   if (o_out && (overlaps(x, rows_bytes, o_out, rows_bytes) || overlaps(out, rows_bytes, o_out, rows_bytes) ||
                 kv8_overlaps(c, o_out, rows_bytes)))
     return VG_ERR_INVALID_ARG;

@@ -465,7 +465,7 @@ typedef struct vg_kv8 {
  * n_new[b] outside [0, rows] or pos[b] + n_new[b] > L_max records
  * VG_ERR_DEVICE_BOUNDS and leaves that sequence as it was. k and v 16-byte
  * aligned, strides a multiple of 8 and at least n_kv * dim; neither may overlap
- * the cache. One launch. Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED,
+ * the cache, and no two of the cache's four parts may share memory. One launch. Errors: VG_ERR_INVALID_ARG, VG_ERR_UNSUPPORTED,
  * VG_ERR_CUDA. */
 vg_status vg_kv8_append(const vg_kv8* c, int32_t rows, const void* k, int64_t k_stride, const void* v,
                         int64_t v_stride, const int32_t* pos, const int32_t* n_new, vg_stream_t stream);

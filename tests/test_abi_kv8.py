@@ -172,3 +172,15 @@ def test_handle_lets_its_tensors_go():
         assert all(r() is None for r in held)
     finally:
         gc.enable()
+
+
+def test_writes_refuse_a_cache_whose_parts_share_memory(lib):
+    """Keys and values in one tensor, one magnitude tensor for both, magnitudes
+    inside the codes: what is written for one would lie over the other."""
+    codes, am = 2 * 10 * 256 * 128, 2 * 10 * 4 * 4
+    need = lib.vg_attn_verify_kv8_workspace_bytes(cache(), 3)
+    layer = lambda c: lib.vg_attn_verify_kv8(c, 3, A + 4 * G, A + 5 * G, A + 6 * G, A + 7 * G, A + 8 * G, None, A + 9 * G, need, None)
+    for kw in (dict(v=A), dict(v=A + codes - 16), dict(v=A - codes + 16), dict(v_amax=A + 2 * G), dict(v_amax=A + 2 * G + am - 4),
+               dict(k_amax=A), dict(k_amax=A + G + codes - 4), dict(v_amax=A + codes - 4), dict(v_amax=A + G)):
+        assert append(lib, cache(**kw)) == 1, kw
+        assert layer(cache(**kw)) == 1, kw
