@@ -406,7 +406,7 @@ def _rows(name, t, n, width, dtypes):
     step, one = t.stride()
     if one != 1 and width > 1:
         raise ValueError(f"{name} must have dense rows")
-    return step if n > 1 else max(step, width)
+    return step if n > 1 else width  # (of a single row it says nothing)
 
 
 def _dense(name, t, shape, dtype):
@@ -451,7 +451,7 @@ def make_kv8(k, v, k_amax, v_amax):
 
 def vg_kv8_append(cache, rows, k, v, pos, n_new=None, stream=None):
     """Quantises `rows` new rows per sequence (k, v: bf16 [B * rows, n_kv * dim],
-    any row stride) into the cache at positions pos[b] .. (the first n_new[b])."""
+    rows a multiple of 8 elements apart) into the cache at positions pos[b] .. (the first n_new[b])."""
     torch = _t()
     B, width, bf16 = cache.B, cache.n_kv * cache.dim, (torch.bfloat16,)
     ks, vs = _rows("k", k, B * rows, width, bf16), _rows("v", v, B * rows, width, bf16)
@@ -485,7 +485,7 @@ def vg_kv8_attn_workspace_bytes(cache, rows, n_heads):
 
 def vg_kv8_attn(cache, rows, n_heads, q, lens, scale, o, workspace, first=None, n_new=None, stream=None):
     """Attention of `rows` query rows per sequence (q, o: bf16 [B * rows,
-    n_heads * dim], any row stride) over the cache."""
+    n_heads * dim], rows a multiple of 8 elements apart) over the cache."""
     torch = _t()
     B, width, bf16 = cache.B, n_heads * cache.dim, (torch.bfloat16,)
     qs, os_ = _rows("q", q, B * rows, width, bf16), _rows("o", o, B * rows, width, bf16)

@@ -184,3 +184,12 @@ def test_writes_refuse_a_cache_whose_parts_share_memory(lib):
                dict(k_amax=A), dict(k_amax=A + G + codes - 4), dict(v_amax=A + codes - 4), dict(v_amax=A + G)):
         assert append(lib, cache(**kw)) == 1, kw
         assert layer(cache(**kw)) == 1, kw
+
+
+def test_row_stride_of_a_single_row():
+    """A single row may come from a matrix of any width: no row lies behind it."""
+    bf16 = torch.bfloat16
+    for wide in (192, 195, 200, 1 << 25):
+        one = torch.empty(1, wide, dtype=bf16, device="meta")[:, :192]
+        assert vgv._rows("k", one, 1, 192, (bf16,)) == 192
+    assert vgv._rows("k", torch.empty(2, 200, dtype=bf16)[:, :192], 2, 192, (bf16,)) == 200

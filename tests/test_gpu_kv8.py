@@ -411,6 +411,27 @@ def test_attention_longest_cache(fmt):
     check_attention(c, 8, 2, [32760, 3])
 
 
+def test_a_single_row_of_an_odd_matrix():
+    """One sequence, one row: columns of a matrix whose rows are no multiple of 8 apart."""
+    c = Cache("int8", 1, 2, 64, 64, 16, seed=18)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(1, 4 * 128 + 3, generator=g, device="cuda").bfloat16()
+    q, k, v, o = (x[:, i * 128:(i + 1) * 128] for i in range(4))
+    plain = [t.contiguous() for t in (q, k, v)]
+    d = Cache("int8", 1, 2, 64, 64, 16, seed=18)
+    ws = torch.zeros(vgv.vg_kv8_attn_workspace_bytes(c.h, 1, 2), dtype=torch.uint8, device="cuda")
+    vgv.vg_kv8_append(c.h, 1, k, v, i32([20]))
+    vgv.vg_kv8_attn(c.h, 1, 2, q, i32([20]), 0.1, o, ws)
+    vgv.vg_kv8_append(d.h, 1, plain[1], plain[2], i32([20]))
+    want, back = torch.zeros_like(plain[0]), torch.zeros(2, 1, 132, device="cuda")
+    vgv.vg_kv8_attn(d.h, 1, 2, plain[0], i32([20]), 0.1, want, ws)
+    vgv.vg_kv8_read(d.h, 1, i32([20]), back[0][:, :128], None)
+    vgv.vg_kv8_read(c.h, 1, i32([20]), back[1][:, :128], None)
+    ok()
+    assert all(torch.equal(c.t[y], d.t[y]) for y in c.t) and torch.equal(o, want) and bool(want.any())
+    assert torch.equal(back[0], back[1]) and bool(back.any()) and not back[:, :, 128:].any()
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^31 codes: the last sequence is written, read and
     attended to."""
