@@ -725,13 +725,16 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
     T += move * (1.0 + mean);
   }
   const double log_s = log(S), lse = (double)m + log_s;
+  // A token with all the mass may come out a rounding of the sums (1e-10) on the
+  // wrong side of 0: what a program takes a logarithm or a root of. NaN stays.
+  auto not_above_0 = [](double x) { return x > 0.0 ? 0.0f : (float)x; };
   if (lane == 0) {
-    if (a.logprob) a.logprob[r] = (float)(z_s[NC] - lse);
-    if (a.entropy) a.entropy[r] = (float)(log_s - T / S);
+    if (a.logprob) a.logprob[r] = not_above_0(z_s[NC] - lse);
+    if (a.entropy) a.entropy[r] = fabsf(not_above_0(T / S - log_s));
   }
   if (lane < NC && rank_s[lane] < a.n_top) {
     a.top_ids[(size_t)r * a.n_top + rank_s[lane]] = id_s[lane];
-    a.top_logprobs[(size_t)r * a.n_top + rank_s[lane]] = (float)(z_s[lane] - lse);
+    a.top_logprobs[(size_t)r * a.n_top + rank_s[lane]] = not_above_0(z_s[lane] - lse);
   }
 }
 

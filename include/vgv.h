@@ -540,7 +540,7 @@ vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* x, const vo
  *   tokens   int32 [R], or NULL if logprob is NULL. A negative token (the padding
  *            of out_tokens) stands for none: its logprob is -inf. One >= V gives
  *            -inf and records VG_ERR_DEVICE_BOUNDS.
- *   logprob, entropy  fp32 [R], each may be NULL
+ *   logprob, entropy  fp32 [R], each may be NULL; no logprob above 0, no entropy below
  *   top_ids, top_logprobs  int32 and fp32 [R, n_top], n_top 0 .. 20, at most V
  * NaN logits make the row's log probabilities and entropy NaN and take no place
  * among the alternatives; where fewer than n_top logits are above -inf the rest

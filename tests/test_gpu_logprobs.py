@@ -374,3 +374,18 @@ def test_hardly_more_tokens_than_candidates(V, H):
     want = lp[np.arange(64), tok]
     assert (np.abs(en - ent) <= tol + 2.0 ** -24 * ent).all(), float((np.abs(en - ent) / tol).max())
     assert (np.abs(got - want) <= tol + 2.0 ** -24 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("H,V,R", [(1280, 5000, 130), (8192, 3000, 64), (64, 1, 5), (1280, 40, 64)])
+def test_no_probability_above_1(H, V, R):
+    """Rows whose token has all the mass but for 1e-10 and less: no log probability
+    above 0, no entropy below it, and none of them negative zero or NaN."""
+    g = np.random.default_rng(H + V)
+    lm = oracle.round_bf16_bits(g.normal(0, 1.2 / np.sqrt(H), (V, H)))
+    tok = g.integers(0, V, R).astype(np.int32)
+    w = oracle.widen(lm)[tok]
+    h = oracle.round_bf16_bits(g.uniform(20, 60, (R, 1)) * w / (w * w).sum(1, keepdims=True))
+    lp, en, _, tl = call(dev(h), dev(lm), torch.from_numpy(tok).cuda(), min(V, 5))
+    assert (lp <= 0).all() and (tl <= 0).all() and (en >= 0).all() and not np.signbit(en).any()
+    assert (lp > -1e-3).mean() > 0.9  # the test's point
+    assert np.array_equal(lp, tl[:, 0])
