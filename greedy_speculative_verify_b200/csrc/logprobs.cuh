@@ -57,9 +57,10 @@ __host__ __device__ constexpr int lp_smem_bytes(int b_rows, int stages) {
   return 1024 + stages * lp_stage_bytes(b_rows) + kLpAux + kLpPend * kLpM * 8;
 }
 
-// Candidates kept for n alternatives: n + kLpSpare rounded up to a size the
+// Candidates kept for n alternatives: n + kLpSpare or more, of the two sizes that the
 // kernels are built for.
-__host__ __device__ constexpr int lp_cands(int n_top) { return n_top <= 8 ? 12 : 24; }
+__host__ __device__ constexpr int lp_cands(int n_top) { return n_top + kLpSpare <= 12 ? 12 : 24; }
+static_assert(lp_cands(kLpMaxTop) >= kLpMaxTop + kLpSpare);
 
 // A row's best logits so far, descending (equal ones by index), in registers.
 template <int NC>
@@ -512,6 +513,7 @@ struct LpFinishArgs {
 
 constexpr int kLpMaxGroups = 512;
 constexpr int kLpFix = 12;  // candidates whose exact logits enter the sums: the same however many alternatives are asked for
+static_assert(kLpFix <= lp_cands(0));
 
 // One CTA per row. The best NC candidates of all units: the NC-th largest of the
 // units' first ones bounds them from below, so at most NC lists have any, and a
