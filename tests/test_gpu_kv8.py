@@ -502,6 +502,59 @@ def test_layer_on_an_8_bit_cache(fmt):
         lens = lens + np.array([1, 2, 4])  # accepted 0, 1 and 3 drafts
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_layer_against_the_codes_it_wrote(fmt):
+    """vg_attn_verify_kv8 in its three parts: the codes and magnitudes of the new
+    rows against the rotated rows of the bf16 layer's oracle, the heads' output
+    against exact attention over those codes, the result against the projection of
+    that output."""
+    H, B, K, L, block = DIMS.H, 4, 3, 384, 64
+    g = np.random.default_rng(22)
+    wqkv = oracle.round_bf16_bits(g.normal(0, 0.02, (3 * H, H)))
+    wo = oracle.round_bf16_bits(g.normal(0, 0.05, (H, H)))
+    c = Cache(fmt, B, 10, L, 128, block, fill=False)
+    lens = [0, 61, 64, 300]
+    c.append(300, [0] * B, lens)
+    ok()
+    before = {y: c.amax[y].copy() for y in "kv"}
+    x = oracle.round_bf16_bits(g.normal(0, 1, (B * (K + 1), H)))
+    ws = torch.zeros(vgv.vg_attn_verify_kv8_workspace_bytes(c.h, K), dtype=torch.uint8, device="cuda")
+    out = torch.empty(B * (K + 1), H, dtype=torch.bfloat16, device="cuda")
+    o = torch.empty_like(out)
+    vgv.vg_attn_verify_kv8(c.h, K, dev(x), dev(wqkv), dev(wo), i32(lens), out, ws, o_out=o)
+    ok()
+    c.gd.check()
+    _, rows, mid = oracle.attn_verify(x, wqkv, wo, np.zeros((B, 2, L, H), np.uint16), lens, K)
+    ez = 6 * np.sqrt(H) * 2.0 ** -23 * (np.abs(oracle.widen(x)) @ np.abs(oracle.widen(wqkv)).T).max()
+    rows = oracle.widen(rows).reshape(B, 2, L, 10, 128).transpose(1, 0, 3, 2, 4)  # [k, v][B, head, position, dim]
+    for y, ref in zip("kv", rows):
+        c.codes[y] = kv8.unpack(c.t[y].cpu().numpy(), fmt, y == "v")
+        c.amax[y] = c.t[y + "a"].cpu().numpy().astype(np.float64)
+        val = kv8.values(np.nan_to_num(c.codes[y]), c.amax[y], block, fmt)
+        for b, n in enumerate(lens):
+            new, a = ref[b, :, n:n + K + 1], np.repeat(c.amax[y][b], block, 1)[:, n:n + K + 1, None]
+            # rows: the projection is an fp32 sum (off by ez at most) rounded to bf16, so both may be a step apart
+            # (2^-7 of the element); rotated, that is up to sqrt(2) steps of the larger element of a pair, and the
+            # second rounding adds one more
+            pair = np.abs(new).reshape(10, K + 1, 64, 2).max(3).repeat(2, 2)
+            off = 2.5 * 2.0 ** -7 * pair + 1.5 * ez
+            # codes: half a step
+            half = a / 254 if fmt == "int8" else np.maximum((np.abs(new) + off) * 2.0 ** -4, a / 448 * 2.0 ** -10)
+            assert (np.abs(val[b, :, n:n + K + 1] - new) <= half * 1.001 + off).all(), (y, b)
+            # magnitudes: the larger one of the block's and the new rows'
+            for k in range(n // block, (n + K) // block + 1):
+                lo, hi = max(n, k * block) - n, min(n + K + 1, (k + 1) * block) - n
+                top = np.abs(new[:, lo:hi]).max((1, 2))
+                top = np.maximum(top, before[y][b, :, k]) if n > k * block else top
+                assert (np.abs(c.amax[y][b, :, k] - top) <= 2.5 * 2.0 ** -7 * top + 1.5 * ez).all(), (y, b, k)
+    k, v = c.values()
+    ref, _, _ = kv8.attention(oracle.widen(mid["q"]).reshape(B, K + 1, 10, 128), k, v, lens, 128 ** -0.5)
+    got = oracle.widen(si.torch_to_bits(o))
+    assert row_rel_err(got, ref.reshape(-1, H)) <= ACT_TOL
+    proj = oracle.round_bf16_bits(got @ oracle.widen(wo).T)
+    assert row_rel_err(oracle.widen(si.torch_to_bits(out)), oracle.widen(x) + oracle.widen(proj)) <= ACT_TOL
+
+
 def test_layer_overflow_leaves_x():
     H, B, K = DIMS.H, 2, 3
     c = Cache("int8", B, 10, 16, 128, 16, seed=22)

@@ -389,3 +389,74 @@ def test_no_probability_above_1(H, V, R):
     assert (lp <= 0).all() and (tl <= 0).all() and (en >= 0).all() and not np.signbit(en).any()
     assert (lp > -1e-3).mean() > 0.9  # the test's point
     assert np.array_equal(lp, tl[:, 0])
+
+
+@pytest.mark.parametrize("R,V,n_top", [(4, 30000, 5), (128, 30000, 20), (300, 9001, 8)])
+def test_captured_calls_equal_eager_ones(R, V, n_top):
+    """Two graphs with workspaces of their own, replayed side by side on two
+    streams with new inputs in the same buffers: the bits of eager calls, one CTA
+    and pairs of CTAs a row block."""
+    H = 128
+    def program():
+        h, lm = (torch.zeros(n, H, dtype=torch.bfloat16, device="cuda") for n in (R, V))
+        t = [torch.zeros(R, device="cuda") for _ in "ab"] + [torch.zeros(R, n_top, dtype=d, device="cuda") for d in (torch.int32, torch.float32)]
+        ws = torch.zeros(vgv.vg_token_logprobs_workspace_bytes(R, H, V, n_top), dtype=torch.uint8, device="cuda")
+        return h, lm, torch.zeros(R, dtype=torch.int32, device="cuda"), t, ws
+
+    def step(p):
+        vgv.vg_token_logprobs(p[0], p[1], p[2], *p[3], p[4])
+
+    eager, graphs = program(), []
+    for _ in range(2):
+        p, stream, gr = program(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.stream(stream):
+            step(p)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(gr, stream=stream):
+            step(p)
+            step(p)  # one call behind the other in the graph, in one workspace
+        graphs.append((p, stream, gr))
+    for seed in range(3):
+        want = []
+        for i, (p, _, _) in enumerate(graphs):
+            h, lm, tok = inputs(R, H, V, seed=10 * seed + i, sure=6.0)
+            for q in (p, eager):
+                q[0].copy_(dev(h)), q[1].copy_(dev(lm)), q[2].copy_(torch.from_numpy(tok))
+            step(eager)
+            want.append([x.clone() for x in eager[3]])
+        torch.cuda.synchronize()
+        for _, stream, gr in graphs:
+            with torch.cuda.stream(stream):
+                gr.replay()
+        torch.cuda.synchronize()
+        assert vgv.vg_get_device_status()[0] == 0
+        for (p, _, _), w in zip(graphs, want):
+            assert all(torch.equal(x, y) for x, y in zip(p[3], w)), seed
+    assert not torch.equal(want[0][0], want[1][0])
+
+
+def test_logits_that_the_tensor_cores_sum_exactly():
+    """Products and partial sums are whole numbers below 2^24 (times a power of
+    two): no logit falls short, nothing is put back, and the sums' own roundings
+    are all that is off. A unit has at most 256 columns here, 16 chunks of 16: chains
+    of 16 terms in a chunk and of 16 chunks, and a new maximum in each of them at
+    worst, which multiplies by an exponential (2^-22) and rounds three times, as the
+    units' joining does once."""
+    H, V, R = 8192, 3000, 130
+    g = np.random.default_rng(41)
+    lm = g.integers(-3, 4, (V, H)).astype(np.float64)
+    h = g.integers(-3, 4, (R, H)) * 2.0 ** -6
+    h[::2, :] = np.abs(h[::2, :])  # rows that lean to one side
+    lm[:, :600] += g.integers(-1, 3, (V, 1))
+    tok = g.integers(0, V, R).astype(np.int32)
+    hb, lb = oracle.round_bf16_bits(h), oracle.round_bf16_bits(lm)
+    lp, ent, mag = kv8.logprobs(hb, lb)
+    assert mag.max() * 2 ** 6 < 2 ** 24
+    for rows in (slice(0, 100), slice(0, R)):  # one row block, and two
+        got, en, _, _ = call(dev(hb[rows]), dev(lb), torch.from_numpy(tok[rows]).cuda(), 5)
+        l, e = lp[rows], ent[rows]
+        p, d = np.exp(l), np.abs(l - l.max(1, keepdims=True))
+        tol = (p * (1 + d) * (18 * 2.0 ** -22 + d * 2.0 ** -23 + 83 * 2.0 ** -24)).sum(1)
+        want = l[np.arange(len(l)), tok[rows]]
+        assert (np.abs(en - e) <= tol + 2.0 ** -24 * e).all(), float((np.abs(en - e) / tol).max())
+        assert (np.abs(got - want) <= tol + 2.0 ** -24 * np.abs(want)).all()
