@@ -90,7 +90,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
 // ----------------------------------------------------------------- TMA
 // Tile loads of a tensor described by a CUtensorMap (passed as a
 // __grid_constant__ kernel parameter) into shared memory, completing on an
-// mbarrier with a transaction byte count. No multicast anywhere.
+// mbarrier with a transaction byte count. No load is multicast.
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0,
                                             int32_t c1) {
   asm volatile(

@@ -16,13 +16,14 @@
 // their logits and the given token's as sums of exact products in fp64, so that
 // the order of close alternatives is that of the exact dot products and does not
 // depend on the tensor cores' summation; kLpSpare or more candidates beyond n
-// keep one from being lost to fp32 rounding at the border.
+// keep one from being lost at the border to what the tensor cores' sums are off by.
 //
 // Up to 128 rows the LM head's stream bounds it: 60 us for 4 rows (331 MB: 50.4 at
-// copy speed), of which 8 are the finishing kernel's round trips, 68 us for 128
-// rows with 20 alternatives, 63 with up to 8. 4,096 rows: 1.04 to
-// 1.12 ms for 1.36 TFLOP (0.82 at cuBLAS's burst rate, 0.99 at its rate under the
-// power cap), 56 us of it finishing. Two epilogue threads a row, or tensor memory
+// copy speed), of which 8 are the finishing kernel's round trips, 70 us for 128
+// rows with 20 alternatives, 63 with up to 8 (captured in graphs; called without end,
+// under the power cap, 65 and 77). 256 rows with 20: 88. 4,096 rows: 0.98
+// to 1.01 ms, and 1.16 under the power cap, for 1.36 TFLOP (0.82 at cuBLAS's burst
+// rate, 0.99 at its rate under the cap), 56 us of it finishing. Two epilogue threads a row, or tensor memory
 // read a chunk ahead, changed nothing at 4,096 rows and cost 3 to 11 us at 128.
 #pragma once
 #include "common.cuh"
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(192, 1)
           // the tile into the sums, and by then finds the others'. Of 129,280 tokens
           // some 400 reach the bound then, one or two of a CTA's 880; with what a
           // CTA's own tile shows, 70 of them entered its list of 24 (20 alternatives,
-          // 128 rows: 74 us where this takes 68; 256 rows 101 and 89).
+          // 128 rows: 74 us where this took 68; 256 rows 101 and 89).
           float top = -INFINITY;
 #pragma unroll 1
           for (int c0 = 0; c0 < cols; c0 += kLpChunk) {
@@ -519,7 +520,7 @@ static_assert(kLpFix <= lp_cands(0));
 // units' first ones bounds them from below, so at most NC lists have any, and a
 // rank count orders what is left. Their tensor-core logits are replaced by the
 // exact ones in the sums too: the tensor cores cut every partial sum towards
-// zero (about 1.5e-8 of a logit for each 16 products, 1.2e-6 at H = 1,280), which
+// zero (measured: some 1.5e-8 of a logit for each 16 products, 1.2e-6 at H = 1,280), which
 // shifts all logits alike but for their size, so where a few tokens hold the
 // mass, correcting those removes most of the error. The kernel is a chain of round
 // trips (statistics and heads; the lists; the candidates' rows), each with all its
@@ -698,7 +699,9 @@ __global__ void __launch_bounds__(NT) logprob_finish(const LpFinishArgs a) {
   if (warp != 0) return;
   // The other tokens' logits fell short like these, by a share of themselves (the
   // least squares' over the candidates; no more than half a place for each 16
-  // products): their mean logit's worth is put back on their S and T. What is left of
+  // products): their mean logit's worth is put back on their S and T. (The entropy
+  // misses that share of the logits' variance with it, 1.6e-7 of itself at H = 1,280;
+  // for that the epilogue would have to sum e^(z-m) (z-m)^2 too.) What is left of
   // the sums without the candidates is a difference: where these hold all the mass it
   // is rounding alone, a residue of 1e-16 beside one of 1e-8 in T, and their quotient
   // any number. So both are kept within what the other tokens can be: V - kLpFix of

@@ -1619,7 +1619,7 @@ struct LpPlan {
 };
 LpPlan lp_plan(int R, int V, int n_top) {
   using namespace vg;
-  constexpr int kSms = 148;
+  constexpr int kSms = 148;  // of a B200: the workspace's size does not go by the device that asks for it
   LpPlan p{};
   p.n_cand = lp_cands(n_top);
   p.n_mblk = cdiv(R, kLpM);

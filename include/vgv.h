@@ -490,8 +490,10 @@ vg_status vg_kv8_read(const vg_kv8* c, int32_t rows, const int32_t* pos, const i
  * h / (n_heads / n_kv), at most 16 to a head. Rows i >= n_new[b] (n_new NULL:
  * none) are not read and get o = 0. lens[b] < 0, first[b] < 0, n_new[b] outside
  * [0, rows] or lens[b] + n_new[b] > L_max records VG_ERR_DEVICE_BOUNDS and gives
- * o = 0 for that sequence. scale > 0; of a row with scores beyond the fp32
- * range nothing is promised; a row with a NaN gives NaN, unless it sees nothing.
+ * o = 0 for that sequence. scale > 0; where scale * max|q| of a row, or that times
+ * the largest key magnitude, reaches 2^118 nothing is promised for the row, and its
+ * scores lose bits where scale * max|q| is below 2^-103. A row with a NaN gives NaN,
+ * unless it sees nothing.
  * Precision: codes enter both products exactly (f16 operands, fp32 sums), query
  * rows exactly down to 2^-29 of their largest element; softmax weights are
  * rounded to 2^-11 of themselves (those that, times their block's share of the
@@ -511,7 +513,9 @@ vg_status vg_kv8_attn(const vg_kv8* c, int32_t rows, int32_t n_heads, const void
  * the cache's): the same layer, with the new rows' k (rotated) and v quantised
  * into the cache (vg_kv8_append at positions lens[b] ..) and the rows' attention
  * read from it (vg_kv8_attn, scale 1/sqrt(128); the workspace is zero-filled
- * before its first call, as there). Arguments and errors otherwise as there;
+ * before its first call, as there). The projections' weights are requested while
+ * earlier kernels of this library on the stream are still running: w_qkv and w_o
+ * must not be what one of those writes. Arguments and errors otherwise as there;
  * unlike there, an overflowing sequence's two device errors share the status
  * word. */
 size_t vg_attn_verify_kv8_workspace_bytes(const vg_kv8* c, int32_t K);
@@ -529,12 +533,16 @@ vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* x, const vo
  *   entropy[r] = lse[r] - sum_v exp(z[r,v] - lse[r]) z[r,v]        (nats)
  *   top_ids[r, 0 .. n_top-1]      = the n_top largest z[r,v], equal ones by lower v
  *   top_logprobs[r, j]            = z[r, top_ids[r,j]] - lse[r]
- * The logits are never stored. lse and the entropy come from tensor-core logits
- * (fp32 sums, which fall short by up to 1e-8 of a logit for 16 products: that is
- * put back by what the largest logits fell short of their exact values); the given tokens' and the alternatives' logits are recomputed as
- * exact products summed in fp64, so the order of close alternatives is that of
- * the exact logits (an alternative can be missed only if more than four others
- * lie within fp32 rounding of the n_top-th).
+ * The logits are never stored. lse and the entropy come from tensor-core logits:
+ * fp32 sums that fall short, typically by 1.5e-8 of a logit for each 16 products
+ * (1.2e-6 at H = 1280). The largest logits enter with their exact values instead,
+ * and what they fell short of those, as a share, is put back on the others. The
+ * given tokens' and the alternatives' logits are recomputed as exact products
+ * summed in fp64, so the order of close alternatives is that of the exact logits.
+ * (Which ones are recomputed, four or more beyond n_top, goes by the tensor-core
+ * logits: an alternative can be missed only if more than four others lie within
+ * what such sums are off by, a few 2^-23 of the sum of the products' magnitudes,
+ * of the n_top-th.)
  *   h        bf16 [R, H], H a multiple of 64, at most 8192
  *   lm_head  bf16 [V, H]
  *   tokens   int32 [R], or NULL if logprob is NULL. A negative token (the padding
@@ -544,7 +552,10 @@ vg_status vg_attn_verify_kv8(const vg_kv8* c, int32_t K, const void* x, const vo
  *   top_ids, top_logprobs  int32 and fp32 [R, n_top], n_top 0 .. 20, at most V
  * NaN logits make the row's log probabilities and entropy NaN and take no place
  * among the alternatives; where fewer than n_top logits are above -inf the rest
- * have id -1. R = 0 is a no-op. Two launches; workspace:
+ * have id -1. R = 0 is a no-op. Two launches, and above 128 rows a memset before
+ * them. The first launch starts streaming the LM head while earlier kernels of this
+ * library on the stream are still running, and reads everything else only after
+ * them: lm_head must not be what one of those writes. Workspace:
  * vg_token_logprobs_workspace_bytes(R, H, V, n_top) bytes, 16-byte aligned,
  * ZERO-FILLED before its first call; every call leaves what has to be zero so,
  * for later calls (one at a time) of any shape, but not for other functions'.
